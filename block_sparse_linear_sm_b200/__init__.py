@@ -28,6 +28,9 @@ SLA_ERR_DEVICE_CHECK = 6
 SLA_MODE_THREEWAY = 0
 SLA_MODE_TOPN_WINDOW = 1
 
+SLA_CACHE_E4M3 = 0
+SLA_CACHE_INT8 = 1
+
 
 class sla_config(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in
@@ -35,6 +38,16 @@ class sla_config(ctypes.Structure):
                  "window", "causal", "has_proj", "proj_per_head", "has_gate", "smooth_k",
                  "linear_all", "cos_filter")] + [("scale", ctypes.c_float), ("cos_theta", ctypes.c_float)] + \
         [(n, ctypes.c_int32) for n in ("nsa_branches", "cmp_block", "cmp_stride")]
+
+
+class sla_cache_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "H", "H_kv", "d", "n_pages", "max_blocks", "kind")] + \
+        [("scale", ctypes.c_float)]
+
+
+class sla_cache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in
+                ("k", "v", "k_scale", "v_scale", "k_mean", "weight", "block_table", "status")]
 
 
 class SlaError(RuntimeError):
@@ -104,6 +117,21 @@ def lib() -> ctypes.CDLL:
         L.sla_route_noalloc.restype = ctypes.c_int
         L.sla_route_noalloc_status.argtypes = [P, ctypes.POINTER(I32)]
         L.sla_route_noalloc_status.restype = ctypes.c_int
+        CC, CM = ctypes.POINTER(sla_cache_config), ctypes.POINTER(sla_cache)
+        L.sla_cache_validate_config.argtypes = [CC]
+        L.sla_cache_validate_config.restype = ctypes.c_int
+        L.sla_cache_append.argtypes = [P, P, CC, CM, I32, P, P, P, P]
+        L.sla_cache_append.restype = ctypes.c_int
+        L.sla_cache_route.argtypes = [P, CC, CM, I32, P, P, I32, P, P]
+        L.sla_cache_route.restype = ctypes.c_int
+        L.sla_cache_attend_workspace_bytes.argtypes = [CC, I32, I32, I32, I32]
+        L.sla_cache_attend_workspace_bytes.restype = S
+        L.sla_cache_attend.argtypes = [P, CC, CM, I32, P, P, P, I32, I32, P, P, S, P]
+        L.sla_cache_attend.restype = ctypes.c_int
+        L.sla_cache_evict_workspace_bytes.argtypes = [CC, I32]
+        L.sla_cache_evict_workspace_bytes.restype = S
+        L.sla_cache_evict.argtypes = [CC, CM, P, I32, I32, I32, P, P, P, P, P, S, P]
+        L.sla_cache_evict.restype = ctypes.c_int
         _lib = L
     return _lib
 
@@ -325,6 +353,191 @@ def sla_permute_tokens(x, y, order, inverse: bool = False, stream=None) -> None:
     rows = x.numel() // (n_tok * d)
     _check(lib().sla_permute_tokens(_ptr(x), _ptr(y), _ptr(order), order.numel(), rows, n_tok, d,
                                     1 if inverse else 0, _stream(stream)), "sla_permute_tokens")
+
+
+# ---------------------------------------------------------------------------
+# serving the top-n mode: the paged 8-bit cache
+# ---------------------------------------------------------------------------
+
+def make_cache_config(c) -> sla_cache_config:
+    """sla_cache_config from any object with the same field names (e.g. workloads.CacheConfig)."""
+    cfg = sla_cache_config()
+    for name, _ in sla_cache_config._fields_:
+        setattr(cfg, name, getattr(c, name))
+    return cfg
+
+
+def _cache_cfg(c) -> sla_cache_config:
+    return c if isinstance(c, sla_cache_config) else make_cache_config(c)
+
+
+def _typed(x, name: str, shape, dtypes, device):
+    """x's address, after checking what the kernels take for granted of it."""
+    if x is None:
+        return None
+    if tuple(x.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(x.shape)}, expected {tuple(shape)}")
+    if x.dtype not in dtypes:
+        raise ValueError(f"{name}: dtype {x.dtype}, expected {' or '.join(map(str, dtypes))}")
+    if x.device != device:
+        raise ValueError(f"{name}: on {x.device}, the cache is on {device}")
+    if not x.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    return x.data_ptr()
+
+
+class SlaCache:
+    """The buffers of a paged 8-bit cache (sla_cache in include/sla.h). The tensors may be
+    changed in place but not replaced: the addresses are taken once.
+
+    k, v          1-byte dtype [n_pages, H_kv, 64, d]
+    k_scale, v_scale  float32 [n_pages, H_kv]
+    k_mean        float32 [n_pages, H_kv, d] or None (sla_cache_route needs it)
+    weight        float32 [B, H_kv, 64 * max_blocks] or None (sla_cache_evict needs it;
+                  sla_cache_attend adds to it when it is there)
+    block_table   int32 [B, max_blocks]
+    status        int32 [64], zeroed once (sla_check_device_status(cache.status) reads it)
+    """
+
+    __slots__ = ("k", "v", "k_scale", "v_scale", "k_mean", "weight", "block_table", "status", "device", "kind",
+                 "shape", "_c")
+
+    def __init__(self, k, v, k_scale, v_scale, k_mean, weight, block_table, status):
+        import torch
+        if not k.is_cuda:
+            raise ValueError("tensor must live on a CUDA device")
+        if k.dim() != 4 or block_table.dim() != 2:
+            raise ValueError("k: 4 dimensions expected, block_table: 2")
+        n_pages, H_kv, block, d = k.shape
+        B, max_blocks = block_table.shape
+        bytes_, f32, i32 = (torch.uint8, torch.int8, torch.float8_e4m3fn), (torch.float32,), (torch.int32,)
+        dev = k.device
+        c = sla_cache()
+        c.k = _typed(k, "k", (n_pages, H_kv, 64, d), bytes_, dev)
+        c.v = _typed(v, "v", (n_pages, H_kv, 64, d), bytes_, dev)
+        c.k_scale = _typed(k_scale, "k_scale", (n_pages, H_kv), f32, dev)
+        c.v_scale = _typed(v_scale, "v_scale", (n_pages, H_kv), f32, dev)
+        c.k_mean = _typed(k_mean, "k_mean", (n_pages, H_kv, d), f32, dev)
+        c.weight = _typed(weight, "weight", (B, H_kv, 64 * max_blocks), f32, dev)
+        c.block_table = _typed(block_table, "block_table", (B, max_blocks), i32, dev)
+        c.status = _typed(status, "status", (64,), i32, dev)
+        self.k, self.v, self.k_scale, self.v_scale, self.k_mean = k, v, k_scale, v_scale, k_mean
+        self.weight, self.block_table, self.status = weight, block_table, status
+        self.device, self._c = dev, c
+        # the element type where the dtype names one (uint8 holds either)
+        self.kind = {torch.int8: SLA_CACHE_INT8, torch.float8_e4m3fn: SLA_CACHE_E4M3}.get(k.dtype)
+        if v.dtype != k.dtype:
+            raise ValueError("k and v must have the same dtype")
+        self.shape = (B, H_kv, d, n_pages, max_blocks)
+
+    @classmethod
+    def empty(cls, c, device="cuda", weight: bool = True, k_mean: bool = True) -> "SlaCache":
+        """A zeroed cache for c whose block table has no page yet (-1 everywhere)."""
+        import torch
+        dt = torch.float8_e4m3fn if c.kind == SLA_CACHE_E4M3 else torch.int8
+
+        def zeros(*shape, dtype=torch.float32):
+            return torch.zeros(*shape, dtype=dtype, device=device)
+
+        return cls(k=zeros(c.n_pages, c.H_kv, 64, c.d, dtype=torch.uint8).view(dt),
+                   v=zeros(c.n_pages, c.H_kv, 64, c.d, dtype=torch.uint8).view(dt),
+                   k_scale=zeros(c.n_pages, c.H_kv), v_scale=zeros(c.n_pages, c.H_kv),
+                   k_mean=zeros(c.n_pages, c.H_kv, c.d) if k_mean else None,
+                   weight=zeros(c.B, c.H_kv, 64 * c.max_blocks) if weight else None,
+                   block_table=torch.full((c.B, c.max_blocks), -1, dtype=torch.int32, device=device),
+                   status=zeros(64, dtype=torch.int32))
+
+
+def _cache_call(c, cache: SlaCache) -> sla_cache_config:
+    """The configuration, after checking that it describes the cache and that the cache's
+    device is the current one (the library launches on the current device)."""
+    import torch
+    cfg = _cache_cfg(c)
+    if (cfg.B, cfg.H_kv, cfg.d, cfg.n_pages, cfg.max_blocks) != cache.shape:
+        raise ValueError(f"the configuration's (B, H_kv, d, n_pages, max_blocks) "
+                         f"{(cfg.B, cfg.H_kv, cfg.d, cfg.n_pages, cfg.max_blocks)} are not the cache's {cache.shape}")
+    if cache.kind is not None and cache.kind != cfg.kind:
+        raise ValueError("the configuration's kind is not the cache's dtype")
+    if cache.device.index != torch.cuda.current_device():
+        raise ValueError(f"the cache is on {cache.device}, the current device is cuda:{torch.cuda.current_device()}")
+    return cfg
+
+
+def _ws_args(ws, device):
+    if ws.device != device:
+        raise ValueError(f"ws: on {ws.device}, the cache is on {device}")
+    return _ptr(ws), ws.numel() * ws.element_size()
+
+
+def sla_cache_validate_config(c) -> int:
+    return lib().sla_cache_validate_config(ctypes.byref(_cache_cfg(c)))
+
+
+def sla_cache_append(k, v, c, cache: SlaCache, lens, n_new=None, lens_out=None, stream=None) -> None:
+    """Writes the first n_new[b] rows of k, v (bf16 [B, H_kv, T, d]) behind lens[b] cached tokens."""
+    import torch
+    cfg = _cache_call(c, cache)
+    dev, bf16, i32 = cache.device, (torch.bfloat16,), (torch.int32,)
+    T = k.shape[2] if k.dim() == 4 else -1
+    _check(lib().sla_cache_append(
+        _typed(k, "k", (cfg.B, cfg.H_kv, T, cfg.d), bf16, dev), _typed(v, "v", (cfg.B, cfg.H_kv, T, cfg.d), bf16, dev),
+        ctypes.byref(cfg), ctypes.byref(cache._c), T, _typed(lens, "lens", (cfg.B,), i32, dev),
+        _typed(n_new, "n_new", (cfg.B,), i32, dev), _typed(lens_out, "lens_out", (cfg.B,), i32, dev),
+        _stream(stream)), "sla_cache_append")
+
+
+def sla_cache_route(q, c, cache: SlaCache, lens, n_new, sel, stream=None) -> None:
+    """The top_n = sel.shape[2] past blocks of a step's queries q (bf16 [B, H, T, d])."""
+    import torch
+    cfg = _cache_call(c, cache)
+    dev, i32 = cache.device, (torch.int32,)
+    T = q.shape[2] if q.dim() == 4 else -1
+    top_n = sel.shape[2] if sel.dim() == 3 else -1
+    _check(lib().sla_cache_route(
+        _typed(q, "q", (cfg.B, cfg.H, T, cfg.d), (torch.bfloat16,), dev), ctypes.byref(cfg), ctypes.byref(cache._c),
+        T, _typed(lens, "lens", (cfg.B,), i32, dev), _typed(n_new, "n_new", (cfg.B,), i32, dev), top_n,
+        _typed(sel, "sel", (cfg.B, cfg.H_kv, top_n), i32, dev), _stream(stream)), "sla_cache_route")
+
+
+def sla_cache_attend_workspace_bytes(c, T: int, top_n: int = 0, window: int = 0, with_weight: bool = False) -> int:
+    return int(lib().sla_cache_attend_workspace_bytes(ctypes.byref(_cache_cfg(c)), T, top_n, window,
+                                                      1 if with_weight else 0))
+
+
+def sla_cache_attend(q, c, cache: SlaCache, lens, n_new, sel, window, out, ws, stream=None) -> None:
+    """Attention of a step's queries q (bf16 [B, H, T, d]) over the cache: all of it (sel None,
+    window 0), the last `window` tokens (sel None), or the blocks in sel and the window."""
+    import torch
+    cfg = _cache_call(c, cache)
+    dev, bf16, i32 = cache.device, (torch.bfloat16,), (torch.int32,)
+    T = q.shape[2] if q.dim() == 4 else -1
+    top_n = 0 if sel is None else sel.shape[2] if sel.dim() == 3 else -1
+    ws_ptr, ws_bytes = _ws_args(ws, dev)
+    _check(lib().sla_cache_attend(
+        _typed(q, "q", (cfg.B, cfg.H, T, cfg.d), bf16, dev), ctypes.byref(cfg), ctypes.byref(cache._c), T,
+        _typed(lens, "lens", (cfg.B,), i32, dev), _typed(n_new, "n_new", (cfg.B,), i32, dev),
+        _typed(sel, "sel", (cfg.B, cfg.H_kv, top_n), i32, dev), top_n, int(window),
+        _typed(out, "out", (cfg.B, cfg.H, T, cfg.d), bf16, dev), ws_ptr, ws_bytes, _stream(stream)), "sla_cache_attend")
+
+
+def sla_cache_evict_workspace_bytes(c, budget: int) -> int:
+    return int(lib().sla_cache_evict_workspace_bytes(ctypes.byref(_cache_cfg(c)), budget))
+
+
+def sla_cache_evict(c, cache: SlaCache, lens, budget, n_sink, n_recent, dst_table, weight_out, kept, lens_out, ws,
+                    stream=None) -> None:
+    """Cuts every sequence to `budget` tokens, those of largest cache.weight; dst_table (int32
+    [B, ceil(budget / 64)]) names the pages that receive them (the cache's own or new ones)."""
+    import torch
+    cfg = _cache_call(c, cache)
+    dev, i32 = cache.device, (torch.int32,)
+    ws_ptr, ws_bytes = _ws_args(ws, dev)
+    _check(lib().sla_cache_evict(
+        ctypes.byref(cfg), ctypes.byref(cache._c), _typed(lens, "lens", (cfg.B,), i32, dev), int(budget), int(n_sink),
+        int(n_recent), _typed(dst_table, "dst_table", (cfg.B, -(-budget // 64)), i32, dev),
+        _typed(weight_out, "weight_out", (cfg.B, cfg.H_kv, 64 * cfg.max_blocks), (torch.float32,), dev),
+        _typed(kept, "kept", (cfg.B, cfg.H_kv, budget), i32, dev), _typed(lens_out, "lens_out", (cfg.B,), i32, dev),
+        ws_ptr, ws_bytes, _stream(stream)), "sla_cache_evict")
 
 
 def sla_version() -> str:

@@ -1,0 +1,116 @@
+// The 8-bit paged cache: what its kernels share (the view of the buffers, the two code
+// formats, the power-of-two scales, checked lengths and page numbers).
+#pragma once
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+
+namespace sla {
+
+constexpr int kCacheMaxB = 1024;       // sequences: the attention kernel scans their lengths in shared memory
+constexpr int kCacheMaxT = 64;         // query rows of a step and head
+constexpr int kCacheMaxRows = 1024;    // query rows of a step and KV head
+constexpr int kCacheMaxSel = 64;       // selected blocks: two list entries a lane
+constexpr float kCacheMaxAbs = 1.329227995784915873e36f;  // 2^120: larger magnitudes are cut to it
+
+// Buffers and sizes of one call (include/sla.h: sla_cache, sla_cache_config).
+struct CacheView {
+  uint8_t *k, *v;
+  float *k_scale, *v_scale, *k_mean, *weight;
+  const int32_t* table;
+  int* status;
+  int B, H, H_kv, group, d, n_pages, max_blocks, cap, kind;
+  float scale;
+};
+
+sla_status check_cache(const sla_cache_config* c, const sla_cache* m, CacheView* view);
+
+// ---------------------------------------------------------------------------
+// scales: exponent of the least power of two s >= 2^-110 with a <= top * s, top = 448
+// (1.75 * 2^8, e4m3) or 127 (1.984375 * 2^6, int8); a is finite, 0 <= a <= 2^120
+// ---------------------------------------------------------------------------
+template <int KIND>
+__device__ __forceinline__ int scale_exponent(float a) {
+  const uint32_t bits = __float_as_uint(a);
+  const int e = (int)(bits >> 23) - 127;  // a = 1.f * 2^e (a subnormal one ends at the lower limit)
+  const uint32_t f = bits & 0x7fffffu;
+  const int x = KIND == SLA_CACHE_E4M3 ? e - 8 + (f > 0x600000u) : e - 6 + (f > 0x7e0000u);
+  return max(-110, min(120, x));
+}
+__device__ __forceinline__ float exp2_int(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+// ---------------------------------------------------------------------------
+// codes
+// ---------------------------------------------------------------------------
+// four codes of x0 .. x3 (already divided by the scale), x0 in the lowest byte
+template <int KIND>
+__device__ __forceinline__ uint32_t encode4(float x0, float x1, float x2, float x3) {
+  if (KIND == SLA_CACHE_E4M3) {
+    uint16_t lo, hi;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(x1), "f"(x0));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(x3), "f"(x2));
+    return (uint32_t)lo | ((uint32_t)hi << 16);
+  }
+  const uint32_t a = (uint32_t)__float2int_rn(x0) & 255u, b = (uint32_t)__float2int_rn(x1) & 255u;
+  const uint32_t c = (uint32_t)__float2int_rn(x2) & 255u, e = (uint32_t)__float2int_rn(x3) & 255u;
+  return a | (b << 8) | (c << 16) | (e << 24);
+}
+
+// two codes (the low 16 bits of c) as fp16, exactly: |e4m3| <= 448 and its subnormals are
+// fp16 normals or subnormals; |int8| <= 128
+template <int KIND>
+__device__ __forceinline__ uint32_t decode2_f16(uint32_t c) {
+  if (KIND == SLA_CACHE_E4M3) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(c));
+    return r;
+  }
+  // byte ^ 0x80 = code + 128 in the mantissa of 1024 + (code + 128); minus 1152
+  const uint32_t w = __byte_perm(c ^ 0x8080u, 0x64646464u, 0x4140);
+  const __half2 bias = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
+  const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&w), bias);
+  return *reinterpret_cast<const uint32_t*>(&y);
+}
+
+template <int KIND>
+__device__ __forceinline__ void decode4(uint32_t c, float* x) {
+  const uint32_t a = decode2_f16<KIND>(c & 0xffffu), b = decode2_f16<KIND>(c >> 16);
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&a));
+  const float2 g = __half22float2(*reinterpret_cast<const __half2*>(&b));
+  x[0] = f.x;
+  x[1] = f.y;
+  x[2] = g.x;
+  x[3] = g.y;
+}
+
+// ---------------------------------------------------------------------------
+// checked device-side arguments
+// ---------------------------------------------------------------------------
+// cached tokens of sequence b, 0 where the value is out of range (*bad set)
+__device__ __forceinline__ int checked_len(const int32_t* lens, int b, int cap, bool* bad) {
+  const int n = lens[b];
+  if (n < 0 || n > cap) {
+    *bad = true;
+    return 0;
+  }
+  return n;
+}
+// valid query rows of sequence b
+__device__ __forceinline__ int checked_new(const int32_t* n_new, int b, int T, bool* bad) {
+  if (n_new == nullptr) return T;
+  const int n = n_new[b];
+  if (n < 0 || n > T) {
+    *bad = true;
+    return 0;
+  }
+  return n;
+}
+// page of block j of sequence b, -1 (and reported) where the table's number is out of range
+__device__ __forceinline__ int checked_page(const CacheView& c, int b, int j) {
+  const int p = c.table[(size_t)b * c.max_blocks + j];
+  if (p >= 0 && p < c.n_pages) return p;
+  report(c.status, SLA_ERR_DEVICE_CHECK, kDetailCachePage);
+  return -1;
+}
+
+}  // namespace sla

@@ -18,6 +18,10 @@ enum DeviceDetail : int {
   kDetailFlashIndex = 101,      // flash kernel read a block index outside [0, nkb)
   kDetailRouteSelect = 102,    // the exact class-boundary selection lost a block (broken invariant)
   kDetailFlashAlign = 103,     // shared-memory base not 1024-byte aligned
+  kDetailCachePage = 110,      // cache: a page number outside [0, n_pages)
+  kDetailCacheLen = 111,       // cache: a length or a number of new tokens out of range
+  kDetailCacheSel = 112,       // cache: a list entry too large or not above those before it
+  kDetailCacheValue = 113,     // cache: a NaN or a magnitude above 2^120 to be stored
   kDetailTimeout = 200,
   kDetailSelftest = 300,       // the failure-detection self-test's wait ran out (expected)
 };

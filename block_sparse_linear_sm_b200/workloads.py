@@ -96,6 +96,20 @@ class LayerConfig:
         return 4.0 * n * n * self.d * self.H * self.B
 
 
+@dataclass
+class CacheConfig:
+    """Sizes of a paged 8-bit cache (field names of sla_cache_config)."""
+
+    B: int
+    H: int
+    H_kv: int
+    d: int
+    n_pages: int
+    max_blocks: int
+    kind: int = 0                 # 0: e4m3 codes, 1: int8
+    scale: float = 0.0            # 0 -> 1/sqrt(d)
+
+
 def _counts(p_h: float, p_l: float, nkb: int) -> tuple[int, int]:
     return int(math.ceil(p_h * nkb - 1e-9)), int(math.floor(p_l * nkb + 1e-9))
 

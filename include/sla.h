@@ -402,6 +402,158 @@ SLA_API sla_status sla_backward_timed(const void* q, const void* k, const void* 
                                       const void* ws, size_t ws_bytes, void* bws, size_t bws_bytes,
                                       void* stream, void* const* events, int32_t n_events);
 
+/* ------------------------------------------------------------------------------------
+ * Serving the top-n mode: a paged cache of keys and values in 8 bits
+ * ------------------------------------------------------------------------------------
+ * The layer above runs whole sequences. The calls below take over where a sequence is
+ * continued a few tokens at a time: its keys and values stay in a cache, in pages of 64
+ * tokens (the routing's block), 8 bits an element, with one scale for each page and KV
+ * head. sla_cache_append writes tokens into it, sla_cache_route picks a step's blocks as
+ * SLA_MODE_TOPN_WINDOW does, sla_cache_attend attends over it and counts how much
+ * attention each cached token got, and sla_cache_evict keeps the tokens that got most.
+ *
+ * Numbers held. An element is code * scale: the code an e4m3 or an int8 number (-127 ..
+ * 127), the scale a power of two, so that dividing by it and changing it are exact and the
+ * one rounding is the code's (to nearest, ties to even). pow2(a) below is the least power
+ * of two s >= 2^-110 with a <= 448 s (e4m3) or a <= 127 s (int8).
+ *
+ * Conventions. Buffers are the caller's, dense and row-major, in the memory of the device
+ * that is current during the call; all work is enqueued on `stream`; a call can be
+ * captured into a graph (no call looks at device data on the host). Calls that write the
+ * same cache or share a workspace must not overlap on the GPU. Arguments that the host can
+ * see are checked before anything is launched; what only the device sees (lengths, page
+ * numbers, lists, non-finite keys) is checked there: the kernels stay in bounds, leave out
+ * what is wrong and set the cache's status word, which stays set until
+ * sla_check_device_status(status, ...) reads and clears it.
+ */
+typedef enum {
+  SLA_CACHE_E4M3 = 0, /* codes are 8-bit floats with 4 exponent and 3 mantissa bits */
+  SLA_CACHE_INT8 = 1  /* codes are signed 8-bit integers, -127 .. 127 */
+} sla_cache_kind;
+
+typedef struct {
+  int32_t B;          /* sequences, 1 .. 1024 */
+  int32_t H;          /* query heads, H % H_kv == 0, up to 1024 */
+  int32_t H_kv;       /* KV heads; head h reads KV head h / (H / H_kv) */
+  int32_t d;          /* head dimension: 64 or 128 */
+  int32_t n_pages;    /* pages of the pool; n_pages * H_kv * 64 < 2^31 */
+  int32_t max_blocks; /* row length of the block table, 1 .. 4096: a sequence holds up to
+                       * 64 * max_blocks tokens */
+  int32_t kind;       /* sla_cache_kind */
+  float scale;        /* softmax scale; 0 = 1/sqrt(d) */
+} sla_cache_config;
+
+typedef struct {
+  void* k;            /* codes [n_pages, H_kv, 64, d], 16-byte aligned */
+  void* v;
+  float* k_scale;     /* fp32 [n_pages, H_kv] */
+  float* v_scale;
+  float* k_mean;      /* fp32 [n_pages, H_kv, d]: mean key of each full page. NULL: not kept
+                       * (sla_cache_route needs it) */
+  float* weight;      /* fp32 [B, H_kv, 64 * max_blocks]: attention weight each slot has got.
+                       * NULL: not kept (sla_cache_evict needs it) */
+  const int32_t* block_table; /* int32 [B, max_blocks]: page of each block of 64 slots. Only
+                       * entries of blocks in use are looked at. A page that a call writes
+                       * belongs to one block of one sequence; pages that are only read may
+                       * be shared */
+  int32_t* status;    /* 256 bytes, 256-byte aligned, zeroed once by the caller */
+} sla_cache;
+
+/* Checks a configuration without touching any pointer (sizes of 0: SLA_ERR_INVALID_ARG;
+ * sizes beyond the limits above: SLA_ERR_UNSUPPORTED). */
+SLA_API sla_status sla_cache_validate_config(const sla_cache_config* cfg);
+
+/*
+ * Writes the first n_new[b] of T new tokens of each sequence into slots lens[b] ..
+ * lens[b] + n_new[b] - 1.
+ *   k, v      bf16 [B, H_kv, T, d], T >= 1; rows at n_new[b] and beyond are not read
+ *   lens      int32 [B]: cached tokens before the call, 0 .. 64 * max_blocks
+ *   n_new     int32 [B], 0 .. T; NULL: T for every sequence
+ *   lens_out  int32 [B] or NULL: receives lens[b] + n_new[b]; not lens itself
+ * For each block written and KV head, K and V apart: with a the largest magnitude of the
+ * block's new elements, a block whose first slot is written now gets scale pow2(a); an
+ * open one gets scale max(old, pow2(a)), and where that is larger the codes it holds are
+ * rounded again at the new scale. The block's slots behind its last token become 0. A
+ * block that becomes full gets its k_mean, the mean of its 64 stored keys (exact in fp32
+ * but for results below 2^-126). weight becomes 0 in the new slots.
+ * Elements that are NaN are stored as 0 and magnitudes above 2^120 as 2^120, with the
+ * status word set. A sequence whose length or n_new is out of range, or that would outgrow
+ * the table, is left alone with the status word set, lens_out[b] = lens[b]; a block whose
+ * page number is out of range likewise.
+ */
+SLA_API sla_status sla_cache_append(const void* k, const void* v, const sla_cache_config* cfg,
+                                    const sla_cache* cache, int32_t T, const int32_t* lens,
+                                    const int32_t* n_new, int32_t* lens_out, void* stream);
+
+/*
+ * Routing of a step (steps 1-3 of SLA_MODE_TOPN_WINDOW with the step's tokens as the query
+ * block): qbar_h = mean of head h's valid query rows; over the past blocks j <
+ * (lens[b] - n_new[b]) / 64, P_h = softmax_j(qbar_h . k_mean_j * scale); the top_n blocks
+ * of largest sum of P_h over the group's heads, equal sums by lower index. Computed in
+ * fp64, like sla_route.
+ *   q      bf16 [B, H, T, d], 1 <= T <= 64, rows at n_new[b] and beyond not read
+ *   lens   int32 [B]: cached tokens, the step's own included (as after sla_cache_append)
+ *   n_new  int32 [B] or NULL (T): valid query rows, the last n_new[b] cached tokens
+ *   sel    int32 [B, H_kv, top_n], 1 <= top_n <= 64: ascending, -1 behind the last
+ * A past block whose page number is out of range scores -inf and is never picked.
+ */
+SLA_API sla_status sla_cache_route(const void* q, const sla_cache_config* cfg, const sla_cache* cache,
+                                   int32_t T, const int32_t* lens, const int32_t* n_new,
+                                   int32_t top_n, int32_t* sel, void* stream);
+
+/*
+ * Softmax attention of a step's queries over the cache.
+ *   q       bf16 [B, H, T, d], 1 <= T <= 64, T * H / H_kv <= 1024
+ *   lens, n_new  as for sla_cache_route; row t < n_new[b] is the token in slot
+ *           p = lens[b] - n_new[b] + t
+ *   sel     int32 [B, H_kv, top_n] or NULL with top_n = 0
+ *   window  tokens p - window + 1 .. p
+ *   out     bf16 [B, H, T, d]; rows t >= n_new[b] and rows that see nothing become 0
+ * Row t sees the slots s <= p that are
+ *   sel NULL, window 0:  all of them
+ *   sel NULL, window > 0: in the window
+ *   sel given:           in a selected block or in the window (window 0: none)
+ * sel holds block numbers below ceil(lens[b] / 64), ascending; negative entries are passed
+ * over, and one that is too large or not above those before it is left out with the status
+ * word set. With cache->weight, weight[b, hk, s] grows by the probabilities that the
+ * group's heads and the step's rows give slot s (summed in a fixed order: results do not
+ * vary from run to run). Slots at lens[b] and beyond never count, whatever they hold.
+ * ws: sla_cache_attend_workspace_bytes bytes (with_weight: cache->weight is not NULL),
+ * 256-byte aligned, needs no initialisation.
+ */
+SLA_API size_t sla_cache_attend_workspace_bytes(const sla_cache_config* cfg, int32_t T, int32_t top_n,
+                                                int32_t window, int32_t with_weight);
+SLA_API sla_status sla_cache_attend(const void* q, const sla_cache_config* cfg, const sla_cache* cache,
+                                    int32_t T, const int32_t* lens, const int32_t* n_new,
+                                    const int32_t* sel, int32_t top_n, int32_t window, void* out,
+                                    void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Eviction by accumulated attention weight: each sequence of more than `budget` tokens is
+ * cut to budget, every KV head by itself. Kept are the first n_sink slots, the last
+ * n_recent, and of the others those of largest cache->weight (equal weights by lower slot;
+ * a NaN weight counts as -inf). They keep their order and move to slots 0 .. budget - 1;
+ * their codes are rounded again at pow2 of the largest magnitude that each new block
+ * holds, which is exact unless a kept token meets larger ones than it had beside it.
+ *   lens        int32 [B]: cached tokens
+ *   budget      >= 1; n_sink, n_recent >= 0, n_sink + n_recent <= budget
+ *   dst_table   int32 [B, ceil(budget / 64)]: pages that receive the kept tokens. An entry
+ *               is either the sequence's own block_table entry of that place (the cache is
+ *               packed where it is) or a page that no block_table row in use names
+ *   weight_out  fp32 [B, H_kv, 64 * max_blocks]: the kept slots' weights at their new
+ *               places, other places left alone; may be cache->weight
+ *   kept        int32 [B, H_kv, budget]: the slot each kept token had, -1 behind the last
+ *   lens_out    int32 [B]: min(lens[b], budget); not lens itself
+ * A sequence of at most budget tokens moves unchanged to its dst_table pages. Full new
+ * blocks get their k_mean (when kept). budget > 64 * max_blocks: SLA_ERR_INVALID_ARG.
+ * ws: sla_cache_evict_workspace_bytes bytes, 256-byte aligned, needs no initialisation.
+ */
+SLA_API size_t sla_cache_evict_workspace_bytes(const sla_cache_config* cfg, int32_t budget);
+SLA_API sla_status sla_cache_evict(const sla_cache_config* cfg, const sla_cache* cache, const int32_t* lens,
+                                   int32_t budget, int32_t n_sink, int32_t n_recent,
+                                   const int32_t* dst_table, float* weight_out, int32_t* kept,
+                                   int32_t* lens_out, void* ws, size_t ws_bytes, void* stream);
+
 /* Static description of a status code. */
 SLA_API const char* sla_status_string(sla_status s);
 
