@@ -1,140 +1,789 @@
 // sla_cache_attend: softmax attention of a step's queries over the paged 8-bit cache.
+//
+// A step has few query rows (T * H / H_kv of a KV head) and a long cache, so each cached
+// key and value is wanted once, by all rows at a time, and the work is spread along the
+// cache. The unit is a tile: one page of one KV head, for up to 16 query rows. All tiles of
+// all sequences and heads, one (sequence, head, row group) segment after the other, form one
+// line that the CTAs cut into equal runs, so a batch of ragged lengths loads every SM alike
+// and one long sequence uses the whole device. The cut depends on the lengths, which only
+// the device knows: every CTA scans them first. A CTA takes its run with four warps, each
+// of them every fourth tile with its own ring of TMA-loaded pages; at the end of a segment
+// the warps' (max, sum, output) are merged through shared memory and either written out
+// (the CTA had the whole segment) or left as a partial that join_kernel adds up.
+//
+// A warp's tile, by mma.sync m16n8k16 on fp16 (codes are fp16 numbers exactly):
+//   S[16 rows x 64 slots] = Q K^T, k_scale and the softmax scale applied in fp32;
+//   m' = max(m, rowmax S), P = 2^(S - m' + 15) as fp16, l = l 2^(m - m') + 2^-15 sum P;
+//   O = O 2^(m - m') + 2^-15 v_scale * (P V).
+// The 15 keeps P's smallest terms out of fp16's subnormals: a weight of 2^-29 still has 11
+// bits. Q is scaled by a power of two a row so that its largest element is in [2^14, 2^15):
+// bf16 elements down to 2^-28 of it are then fp16 numbers exactly.
+// K's product runs over a permuted d (a lane's 16-byte loads of a key row are its k indices
+// of consecutive steps), V's over permuted slots (the order in which ldmatrix hands out the
+// transposed bytes), with Q's and S's columns permuted alike.
+#include <cuda.h>
+
 #include "cache.cuh"
+#include "tc.cuh"
 
 namespace sla {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kRows = 16;       // query rows of a segment
+constexpr int kSlots = 2;       // pages in a warp's ring
+constexpr int kInfo = 4;        // described tiles ahead (at most kSlots + 1 are in use)
+constexpr int kMinRun = kWarps;  // tiles a CTA takes at least
+constexpr float kShift = 15.f;
 
 struct Step {
   const __nv_bfloat16* q;
   const int32_t *lens, *n_new, *sel;
   __nv_bfloat16* out;
-  float* lse;  // [B, H, T], natural log; -inf where a row sees nothing
-  int T, top_n, window;
+  float* part_ml;   // [slots][2][16]: m, l of a partial
+  float* part_o;    // [slots][16][D]
+  float* lse;       // [B, H, T] log2-sum-exp (with weights)
+  float* scores;    // [tiles of all (sequence, KV head)][rows][64] (with weights)
+  int T, top_n, window, rows, groups;  // rows = T * group of a KV head, in groups of kRows
 };
 
-// Whether block j is in the list, and whether every entry up to its place is in order.
-__device__ bool in_list(const int32_t* list, int n, int j) {
-  int top = -1;
-  for (int i = 0; i < n; ++i) {
-    if (list[i] == j && j > top) return true;
-    top = max(top, list[i]);
-  }
-  return false;
+// ---------------------------------------------------------------------------
+// the line of tiles
+// ---------------------------------------------------------------------------
+// Tiles of one (sequence, KV head): list entries first, then the window's (or all) blocks.
+__device__ __forceinline__ int first_block(const Step& a, int L, int n) {
+  return a.window > 0 ? max(0, L - n - a.window + 1) / kBlock : 0;
+}
+__device__ __forceinline__ int tile_count(const Step& a, int L, int n) {
+  if (n == 0 || L == 0) return 0;
+  const int range = (L + kBlock - 1) / kBlock - first_block(a, L, n);
+  return a.sel == nullptr ? range : a.top_n + (a.window > 0 ? range : 0);
 }
 
-// Score of one row against slot s of (b, hk): a warp, lane holds d/32 elements of q.
-template <int KIND, int D>
-__device__ __forceinline__ float score_of(const CacheView& c, size_t ph, int row, const float* q, int lane) {
-  constexpr int E = D / 32;
-  const uint8_t* p = c.k + (ph * kBlock + row) * D + lane * E;
-  float x[4], a = 0.f;
-  decode4<KIND>(E == 4 ? *reinterpret_cast<const uint32_t*>(p) : *reinterpret_cast<const uint16_t*>(p), x);
+struct Lines {  // in shared memory
+  int* cum;     // [B + 1]: tiles of one KV head of the sequences before
+  int* len;     // [B]
+  uint8_t* fresh;  // [B]: valid query rows of a head
+};
+__host__ __device__ inline size_t lines_bytes(int B) { return align_up((size_t)(2 * B + 1) * 4 + B, 16); }
+
+// All threads of the block; ends with a barrier.
+__device__ void scan_lines(const CacheView& c, const Step& a, char* smem, Lines* out, int* warp_sums) {
+  Lines l;
+  l.cum = reinterpret_cast<int*>(smem);
+  l.len = l.cum + c.B + 1;
+  l.fresh = reinterpret_cast<uint8_t*>(l.len + c.B);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
+  const int per = (c.B + blockDim.x - 1) / blockDim.x, b0 = tid * per;
+  int mine = 0;
+  for (int b = b0; b < min(c.B, b0 + per); ++b) {
+    bool bad = false;
+    const int L = checked_len(a.lens, b, c.cap, &bad), n = checked_new(a.n_new, b, a.T, &bad);
+    if (bad && blockIdx.x == 0) report(c.status, SLA_ERR_DEVICE_CHECK, kDetailCacheLen);
+    l.len[b] = L;
+    l.fresh[b] = (uint8_t)n;
+    const int t = tile_count(a, L, n);
+    l.cum[b] = t;
+    mine += t;
+  }
+  int upto = mine;
 #pragma unroll
-  for (int e = 0; e < E; ++e) a += q[e] * x[e];
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
-  return a * c.k_scale[ph] * c.scale;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += y;
+  }
+  if (lane == 31) warp_sums[warp] = upto;
+  __syncthreads();
+  int before = upto - mine;
+  for (int w = 0; w < nw; ++w)
+    if (w < warp) before += warp_sums[w];
+  for (int b = b0; b < min(c.B, b0 + per); ++b) {
+    const int t = l.cum[b];
+    l.cum[b] = before;
+    before += t;
+  }
+  if (b0 < c.B && b0 + per >= c.B) l.cum[c.B] = before;
+  __syncthreads();
+  *out = l;
 }
 
-// One CTA a query row; its warps take the slots in turn and are merged at the end.
-template <int KIND, int D>
-__global__ void __launch_bounds__(kThreads) attend_kernel(const CacheView c, const Step a) {
-  constexpr int E = D / 32;
-  __shared__ float s_m[kWarps], s_l[kWarps], s_o[kWarps][D];
-  const int h = blockIdx.x % c.H, b = blockIdx.x / c.H, t = blockIdx.y, hk = h / c.group;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  bool bad = false;
-  const int L = checked_len(a.lens, b, c.cap, &bad), n = checked_new(a.n_new, b, a.T, &bad);
-  if (bad && threadIdx.x == 0) report(c.status, SLA_ERR_DEVICE_CHECK, kDetailCacheLen);
-  const int pos = t < n ? L - n + t : -1;
-  const size_t row = (size_t)blockIdx.x * a.T + t;
-  float q[E], o[E] = {}, m = -INFINITY, l = 0.f;
-  for (int e = 0; e < E; ++e) q[e] = __bfloat162float(a.q[row * D + lane * E + e]);
-  const int32_t* list = a.sel ? a.sel + ((size_t)b * c.H_kv + hk) * a.top_n : nullptr;
-  if (list != nullptr && threadIdx.x == 0)
-    for (int i = 0, top = -1; i < a.top_n; ++i) {
-      if (list[i] >= 0 && (list[i] <= top || list[i] >= (L + kBlock - 1) / kBlock))
-        report(c.status, SLA_ERR_DEVICE_CHECK, kDetailCacheSel);
-      top = max(top, list[i]);
-    }
-  for (int j = 0; j * kBlock <= pos; ++j) {
-    const bool chosen = list ? in_list(list, a.top_n, j) : a.window == 0;
-    const int lo = chosen ? 0 : max(0, pos - a.window + 1 - j * kBlock);
-    const int hi = min(kBlock, pos - j * kBlock + 1);
-    if (lo >= hi) continue;
-    const int page = checked_page(c, b, j);
-    if (page < 0) continue;
-    const size_t ph = (size_t)page * c.H_kv + hk;
-    for (int r = lo + warp; r < hi; r += kWarps) {
-      const float s = score_of<KIND, D>(c, ph, r, q, lane);
-      const float top = fmaxf(m, s), keep = __expf(m - top), p = __expf(s - top);
-      const uint8_t* v = c.v + (ph * kBlock + r) * D + lane * E;
-      float x[4];
-      decode4<KIND>(E == 4 ? *reinterpret_cast<const uint32_t*>(v) : *reinterpret_cast<const uint16_t*>(v), x);
-      const float f = p * c.v_scale[ph];
-      for (int e = 0; e < E; ++e) o[e] = o[e] * keep + f * x[e];
-      l = l * keep + p;
-      m = top;
+// Sequence that holds tile t of the line (per: segments a KV-head line of a sequence has).
+__device__ __forceinline__ int find_sequence(const Lines& l, int B, unsigned t, unsigned per) {
+  int lo = 0, hi = B - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if ((unsigned)l.cum[mid] * per <= t) lo = mid;
+    else hi = mid - 1;
+  }
+  // sequences without tiles share their number with the next: the last of them was found
+  return lo;
+}
+
+// Block of tile idx of (b, hk); -1 where it is none. *chosen: the window does not limit it.
+// Called by a whole warp.
+__device__ __forceinline__ int tile_block(const CacheView& c, const Step& a, int b, int hk, int idx, int L, int n,
+                                          int lane, bool* chosen) {
+  const int first = first_block(a, L, n);
+  if (a.sel == nullptr) {
+    *chosen = a.window == 0;
+    return first + idx;
+  }
+  const int32_t* list = a.sel + ((size_t)b * c.H_kv + hk) * a.top_n;
+  const int e0 = lane < a.top_n ? list[lane] : -1, e1 = lane + 32 < a.top_n ? list[lane + 32] : -1;
+  // an entry counts where it is above every earlier one and inside the sequence
+  int p0 = e0, p1 = e1;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y0 = __shfl_up_sync(0xffffffffu, p0, o), y1 = __shfl_up_sync(0xffffffffu, p1, o);
+    if (lane >= o) {
+      p0 = max(p0, y0);
+      p1 = max(p1, y1);
     }
   }
+  const int all0 = __shfl_sync(0xffffffffu, p0, 31);
+  int before0 = __shfl_up_sync(0xffffffffu, p0, 1), before1 = __shfl_up_sync(0xffffffffu, p1, 1);
+  if (lane == 0) before0 = before1 = -1;
+  before1 = max(before1, all0);
+  const int blocks = (L + kBlock - 1) / kBlock;
+  const bool ok0 = e0 >= 0 && e0 > before0 && e0 < blocks, ok1 = e1 >= 0 && e1 > before1 && e1 < blocks;
+  if (idx < a.top_n) {
+    *chosen = true;
+    const int e = __shfl_sync(0xffffffffu, idx < 32 ? e0 : e1, idx & 31);
+    const bool ok = __shfl_sync(0xffffffffu, (int)(idx < 32 ? ok0 : ok1), idx & 31) != 0;
+    if (!ok && e >= 0 && lane == 0) report(c.status, SLA_ERR_DEVICE_CHECK, kDetailCacheSel);
+    return ok ? e : -1;
+  }
+  *chosen = false;
+  const int j = first + idx - a.top_n;
+  return __any_sync(0xffffffffu, (ok0 && e0 == j) || (ok1 && e1 == j)) ? -1 : j;
+}
+
+// ---------------------------------------------------------------------------
+// instructions
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+// Two 16 x 16 byte matrices, transposed: lane (g = lane / 4, q = lane % 4) gets in r[2 i]
+// rows 4 q .. 4 q + 3 of column g of matrix i and in r[2 i + 1] of column g + 8. Lanes
+// 0 - 15 give the row addresses of matrix 0, the others of matrix 1.
+__device__ __forceinline__ void ldmatrix_trans_b8(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void tma_load_rows(uint32_t dst, const CUtensorMap* map, uint32_t bar, int row) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(0), "r"(row)
+      : "memory");
+}
+__device__ __forceinline__ float log2_sum(float m, float l) { return l == 0.f ? -INFINITY : m + log2f(l); }
+
+// ---------------------------------------------------------------------------
+// a warp's ring
+// ---------------------------------------------------------------------------
+struct TileInfo {
+  int seg, block, ph;  // segment of the line, block of the sequence, page * H_kv + hk
+  int tile;            // number of the tile among those of all (sequence, KV head)
+  int chosen;
+};
+
+template <int D>
+struct Ring {
+  static constexpr int kPage = kBlock * D;  // bytes of a page of one head
+  uint32_t data, bars;                      // shared addresses: kSlots pages, kSlots barriers
+  TileInfo* info;                           // [kInfo]
+  unsigned issued, used;                    // pages requested and released (K and V of a tile in turn)
+  unsigned next, end;                       // tiles of the line still to be described
+  int seq;                                  // sequence of tile `next`
+  int vrow;                                 // page whose values are requested next, -1: describe a tile
+};
+
+template <int D>
+__device__ __forceinline__ void request(Ring<D>& r, const CUtensorMap* map, int row, int lane) {
+  const uint32_t slot = r.issued % kSlots;
   if (lane == 0) {
-    s_m[warp] = m;
-    s_l[warp] = l;
+    tc::mbar_expect_tx(r.bars + 8 * slot, Ring<D>::kPage);
+    tma_load_rows(r.data + slot * Ring<D>::kPage, map, r.bars + 8 * slot, row);
   }
+  ++r.issued;
+}
+
+// Requests pages until the ring is full or the run ends. Called by the whole warp, after
+// every lane has finished with the released pages.
+template <int D>
+__device__ __forceinline__ void pump(Ring<D>& r, const CacheView& c, const Step& a, const Lines& l,
+                                     const CUtensorMap* kmap, const CUtensorMap* vmap, int lane) {
+  __syncwarp();
+  while (r.issued - r.used < kSlots) {
+    if (r.vrow >= 0) {
+      request(r, vmap, r.vrow, lane);
+      r.vrow = -1;
+      continue;
+    }
+    if (r.next >= r.end) break;
+    const unsigned per = c.H_kv * a.groups;
+    while ((unsigned)l.cum[r.seq + 1] * per <= r.next) ++r.seq;
+    const int b = r.seq, nb = l.cum[b + 1] - l.cum[b];
+    const unsigned in = r.next - (unsigned)l.cum[b] * per, sr = in / (unsigned)nb;
+    const int hk = (int)sr / a.groups;
+    bool chosen;
+    const int idx = (int)(in - sr * nb);
+    const int j = tile_block(c, a, b, hk, idx, l.len[b], l.fresh[b], lane, &chosen);
+    r.next += kWarps;
+    if (j < 0) continue;
+    const int page = c.table[(size_t)b * c.max_blocks + j];
+    if (page < 0 || page >= c.n_pages) {
+      if (lane == 0) report(c.status, SLA_ERR_DEVICE_CHECK, kDetailCachePage);
+      continue;
+    }
+    const int ph = page * c.H_kv + hk;
+    if (lane == 0) {
+      TileInfo* t = &r.info[(r.issued / 2) % kInfo];
+      t->seg = b * (int)per + (int)sr;
+      t->block = j;
+      t->ph = ph;
+      t->tile = l.cum[b] * c.H_kv + hk * nb + idx;
+      t->chosen = chosen;
+    }
+    request(r, kmap, ph * kBlock, lane);
+    r.vrow = ph * kBlock;
+  }
+  __syncwarp();
+}
+
+// ---------------------------------------------------------------------------
+// the attention kernel
+// ---------------------------------------------------------------------------
+template <int D>
+struct Smem {
+  static constexpr int kRing = kWarps * kSlots * kBlock * D;
+  static constexpr int kMerge = kWarps * kRows * D * 4;
+  static constexpr int off_merge = kRing, off_misc = kRing + kMerge;
+  static constexpr int kMisc = 2048;
+  static constexpr int off_lines = off_misc + kMisc;
+  static size_t bytes(int B) { return off_lines + lines_bytes(B) + 1024; }
+};
+
+template <int KIND, int D>
+__global__ void __launch_bounds__(kThreads, 2)
+    attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const CacheView c,
+                  const Step a) {
+  constexpr int KS = D / 16;  // k steps of Q K^T; words of codes a lane holds of a key row
+  constexpr int NT = D / 8;   // output column tiles
+  extern __shared__ char raw[];
+  char* smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+  struct Misc {
+    uint64_t bars[kWarps][kSlots];
+    TileInfo info[kWarps][kInfo];
+    float m[kWarps][kRows], l[kWarps][kRows];
+    int warp_sums[kWarps];
+    int abort, never;
+  };
+  static_assert(sizeof(Misc) <= Smem<D>::kMisc, "misc");
+  Misc& mi = *reinterpret_cast<Misc*>(smem + Smem<D>::off_misc);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q4 = lane & 3;
+
+  if (tid == 0) {
+    mi.abort = mi.never = 0;
+    for (int w = 0; w < kWarps; ++w)
+      for (int i = 0; i < kSlots; ++i) tc::mbar_init(smem_u32(&mi.bars[w][i]), 1);
+    tc::fence_mbar_init();
+    tc::prefetch_tensormap(&kmap);
+    tc::prefetch_tensormap(&vmap);
+  }
+  Lines l;
+  scan_lines(c, a, smem + Smem<D>::off_lines, &l, mi.warp_sums);
+  asm volatile("griddepcontrol.launch_dependents;");
+
+  // this CTA's run of the line
+  const unsigned per = c.H_kv * a.groups, total = (unsigned)l.cum[c.B] * per;
+  const unsigned run = max((total + gridDim.x - 1) / gridDim.x, (unsigned)kMinRun);
+  const unsigned lo = min(total, blockIdx.x * run), hi = min(total, lo + run);
+  if (lo >= hi) return;
+
+  Ring<D> ring;
+  ring.data = smem_u32(smem) + warp * kSlots * Ring<D>::kPage;
+  ring.bars = smem_u32(&mi.bars[warp][0]);
+  ring.info = mi.info[warp];
+  ring.issued = ring.used = 0;
+  ring.next = lo + warp;
+  ring.end = hi;
+  ring.seq = find_sequence(l, c.B, lo, per);
+  ring.vrow = -1;
+  pump(ring, c, a, l, &kmap, &vmap, lane);
+
+  float* merge = reinterpret_cast<float*>(smem + Smem<D>::off_merge);
+  bool dead = false;
+  unsigned at = lo;  // first tile of the segment being worked on
+  int b = ring.seq;
+  b = find_sequence(l, c.B, lo, per);
+  while (at < hi) {
+    while ((unsigned)l.cum[b + 1] * per <= at) ++b;
+    const int nb = l.cum[b + 1] - l.cum[b], L = l.len[b], n = l.fresh[b];
+    const unsigned sr = (at - (unsigned)l.cum[b] * per) / (unsigned)nb;
+    const int hk = (int)sr / a.groups, grp = (int)sr % a.groups, seg = b * (int)per + (int)sr;
+    const unsigned seg_lo = (unsigned)l.cum[b] * per + sr * nb, seg_hi = seg_lo + nb;
+    const int row0 = grp * kRows;
+    const size_t qrow0 = ((size_t)b * c.H + (size_t)hk * c.group) * a.T;
+
+    // Q: two rows of this lane, row g and g + 8, d = q4 * D / 4 ..
+    uint32_t qf[KS][4];
+    float qs[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = row0 + g + 8 * i;
+      float x[D / 4];
+#pragma unroll
+      for (int e = 0; e < D / 4; ++e) x[e] = 0.f;
+      if (r < a.rows) {
+        const uint4* p = reinterpret_cast<const uint4*>(a.q + (qrow0 + r) * D + q4 * (D / 4));
+#pragma unroll
+        for (int u = 0; u < D / 32; ++u) {
+          const uint4 w = p[u];
+          const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 f = unpack_bf16(ws[e]);
+            x[8 * u + 2 * e] = f.x;
+            x[8 * u + 2 * e + 1] = f.y;
+          }
+        }
+      }
+      float top = 0.f;
+#pragma unroll
+      for (int e = 0; e < D / 4; ++e) top = fmaxf(top, fabsf(x[e]));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const int ex = max((int)(__float_as_uint(top) >> 23) - 127, -100);
+      const float up = exp2_int(14 - ex);
+      qs[i] = exp2_int(ex - 14) * (c.scale * 1.4426950408889634f);
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        qf[s][i] = pack_f16(x[4 * s] * up, x[4 * s + 1] * up);
+        qf[s][i + 2] = pack_f16(x[4 * s + 2] * up, x[4 * s + 3] * up);
+      }
+    }
+    // the slots a row sees end at pos
+    int pos[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = row0 + g + 8 * i, t = r % a.T;
+      pos[i] = r < a.rows && t < n ? L - n + t : -1;
+    }
+
+    float o[NT][4], m[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+
+    while (ring.used < ring.issued) {
+      const TileInfo* ti = &ring.info[(ring.used / 2) % kInfo];
+      if (ti->seg != seg) break;
+      const int j0 = ti->block * kBlock, ph = ti->ph, tile = ti->tile;
+      const bool chosen = ti->chosen;
+      const float ks = c.k_scale[ph], vs = c.v_scale[ph] * exp2_int(-(int)kShift);
+      const uint32_t slot_k = ring.used % kSlots;
+      if (!dead && !tc::mbar_wait(ring.bars + 8 * slot_k, (ring.used / kSlots) & 1, &mi.abort)) dead = true;
+      const uint32_t kbase = ring.data + slot_k * Ring<D>::kPage;
+
+      // scores: column 2 q4 + e of tile 2 t + h is slot 16 t + 4 q4 + 2 h + e
+      float s[8][4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float(&acc)[4] = s[2 * t + h];
+          acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
+          const int row = 16 * t + 4 * (g >> 1) + (g & 1) + 2 * h;
+          uint32_t w[KS];
+          if (D == 128) {
+            const uint32_t at0 = kbase + row * 128;
+            const uint4 x = lds128(at0 + (((2 * q4) ^ (row & 7)) << 4)), y = lds128(at0 + (((2 * q4 + 1) ^ (row & 7)) << 4));
+            w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+            w[KS - 4] = y.x, w[KS - 3] = y.y, w[KS - 2] = y.z, w[KS - 1] = y.w;
+          } else {
+            const uint4 x = lds128(kbase + row * 64 + ((q4 ^ ((row >> 1) & 3)) << 4));
+            w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+          }
+#pragma unroll
+          for (int k = 0; k < KS; ++k)
+            mma_f16(acc, qf[k], decode2_f16<KIND>(w[k] & 0xffffu), decode2_f16<KIND>(w[k] >> 16));
+        }
+      }
+      ++ring.used;
+      pump(ring, c, a, l, &kmap, &vmap, lane);
+
+      const float f0 = qs[0] * ks, f1 = qs[1] * ks;
+#pragma unroll
+      for (int t = 0; t < 8; ++t) {
+        s[t][0] *= f0;
+        s[t][1] *= f0;
+        s[t][2] *= f1;
+        s[t][3] *= f1;
+      }
+      // rows that do not see the whole page: its end, the window's start
+      if (j0 + kBlock - 1 > L - n || (!chosen && j0 <= L - 1 - a.window)) {
+#pragma unroll
+        for (int t = 0; t < 8; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int slot = j0 + 16 * (t >> 1) + 4 * q4 + 2 * (t & 1) + (e & 1), p = pos[e >> 1];
+            if (slot > p || (!chosen && slot <= p - a.window)) s[t][e] = -INFINITY;
+          }
+      }
+      if (a.scores != nullptr) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int r = row0 + g + 8 * i;
+          if (r < a.rows) {
+            float4* p = reinterpret_cast<float4*>(a.scores + ((size_t)tile * a.rows + r) * kBlock) + q4;
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+              p[4 * t] = make_float4(s[2 * t][2 * i], s[2 * t][2 * i + 1], s[2 * t + 1][2 * i], s[2 * t + 1][2 * i + 1]);
+          }
+        }
+      }
+      float alpha[2], base[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float top = m[i];
+#pragma unroll
+        for (int t = 0; t < 8; ++t) top = fmaxf(top, fmaxf(s[t][2 * i], s[t][2 * i + 1]));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        base[i] = top == -INFINITY ? 0.f : top - kShift;
+        alpha[i] = tc::ex2_approx(m[i] - (top == -INFINITY ? 0.f : top));
+        m[i] = top;
+        sum[i] *= alpha[i];
+      }
+      uint32_t pf[4][4];
+#pragma unroll
+      for (int t = 0; t < 8; ++t) {
+        float p[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) p[e] = tc::ex2_approx(s[t][e] - base[e >> 1]);
+        sum[0] += p[0] + p[1];
+        sum[1] += p[2] + p[3];
+        pf[t >> 1][2 * (t & 1)] = pack_f16(p[0], p[1]);
+        pf[t >> 1][2 * (t & 1) + 1] = pack_f16(p[2], p[3]);
+      }
+      if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          o[i][0] *= alpha[0];
+          o[i][1] *= alpha[0];
+          o[i][2] *= alpha[1];
+          o[i][3] *= alpha[1];
+        }
+      }
+
+      const uint32_t slot_v = ring.used % kSlots;
+      if (!dead && !tc::mbar_wait(ring.bars + 8 * slot_v, (ring.used / kSlots) & 1, &mi.abort)) dead = true;
+      const uint32_t vbase = ring.data + slot_v * Ring<D>::kPage;
+      // codes of slots behind the last token are whatever they are: they count as 0
+      uint32_t live[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const int left = L - j0 - 16 * t - 4 * q4;
+        live[t] = left >= 4 ? 0xffffffffu : left <= 0 ? 0u : (1u << (8 * left)) - 1u;
+      }
+#pragma unroll
+      for (int cc = 0; cc < D / 32; ++cc) {
+        float acc[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const int row = 16 * t + (lane & 15), ch = 2 * cc + (lane >> 4);
+          const uint32_t addr = vbase + row * D + ((ch ^ (D == 128 ? (row & 7) : ((row >> 1) & 3))) << 4);
+          uint32_t w[4];
+          ldmatrix_trans_b8(w, addr);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t x = w[i] & live[t];
+            mma_f16(acc[i], pf[t], decode2_f16<KIND>(x & 0xffffu), decode2_f16<KIND>(x >> 16));
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[4 * cc + i][e] += vs * acc[i][e];
+      }
+      ++ring.used;
+      pump(ring, c, a, l, &kmap, &vmap, lane);
+    }
+
+    // the warps' parts of the segment become one
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 1);
+      sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 2);
+      if (q4 == 0) {
+        mi.m[warp][g + 8 * i] = m[i];
+        mi.l[warp][g + 8 * i] = sum[i] * exp2_int(-(int)kShift);
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = g + 8 * i;
+      float top = mi.m[0][r];
+      for (int w = 1; w < kWarps; ++w) top = fmaxf(top, mi.m[w][r]);
+      const float f = tc::ex2_approx(m[i] - (top == -INFINITY ? 0.f : top));
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+        *reinterpret_cast<float2*>(merge + (warp * kRows + r) * D + 8 * t + 2 * q4) =
+            make_float2(o[t][2 * i] * f, o[t][2 * i + 1] * f);
+    }
+    __syncthreads();
+    const bool whole = seg_lo >= lo && seg_hi <= hi;
+    const size_t part = (size_t)blockIdx.x + seg;
+    for (int e = tid; e < kRows * D / 4; e += kThreads) {
+      const int r = e / (D / 4), d4 = e % (D / 4);
+      float4 y = reinterpret_cast<const float4*>(merge)[e];
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) {
+        const float4 x = reinterpret_cast<const float4*>(merge)[w * (kRows * D / 4) + e];
+        y.x += x.x;
+        y.y += x.y;
+        y.z += x.z;
+        y.w += x.w;
+      }
+      float top = mi.m[0][r], all = 0.f;
+      for (int w = 1; w < kWarps; ++w) top = fmaxf(top, mi.m[w][r]);
+      for (int w = 0; w < kWarps; ++w) all += mi.l[w][r] * tc::ex2_approx(mi.m[w][r] - (top == -INFINITY ? 0.f : top));
+      if (!whole) {
+        reinterpret_cast<float4*>(a.part_o)[part * (kRows * D / 4) + e] = y;
+        if (d4 == 0) {
+          a.part_ml[part * 2 * kRows + r] = top;
+          a.part_ml[part * 2 * kRows + kRows + r] = all;
+        }
+      } else if (row0 + r < a.rows) {
+        const float inv = all == 0.f || (row0 + r) % a.T >= n ? 0.f : 1.f / all;
+        uint2 v = make_uint2(pack_bf16(y.x * inv, y.y * inv), pack_bf16(y.z * inv, y.w * inv));
+        if ((row0 + r) % a.T >= n) v = make_uint2(0u, 0u);
+        *reinterpret_cast<uint2*>(a.out + (qrow0 + row0 + r) * D + 4 * d4) = v;
+        if (d4 == 0 && a.lse != nullptr) a.lse[qrow0 + row0 + r] = log2_sum(top, all);
+      }
+    }
+    at = seg_hi;
+    __syncthreads();  // merge, m and l are free again
+  }
+  if (dead) {
+    mi.abort = 1;
+    if (lane == 0) report(c.status, SLA_ERR_DEVICE_TIMEOUT, kDetailTimeout);
+    // copies still on their way land before the block's memory is given back
+    for (unsigned i = ring.issued > kSlots ? ring.issued - kSlots : 0; i < ring.issued; ++i)
+      tc::mbar_wait(ring.bars + 8 * (i % kSlots), (i / kSlots) & 1, &mi.never);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// segments that several CTAs worked on, or none
+// ---------------------------------------------------------------------------
+// One CTA a (segment, row): its warps take the partials in turn, a lane D / 32 columns.
+template <int D>
+__global__ void __launch_bounds__(kThreads) join_kernel(const CacheView c, const Step a, unsigned ctas) {
+  constexpr int E = D / 32;
+  extern __shared__ char raw[];
+  __shared__ int warp_sums[kWarps];
+  __shared__ float s_l[kWarps], s_o[kWarps][D];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  Lines l;
+  scan_lines(c, a, raw, &l, warp_sums);
+  const unsigned per = c.H_kv * a.groups, total = (unsigned)l.cum[c.B] * per;
+  const unsigned run = max((total + ctas - 1) / ctas, (unsigned)kMinRun);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
+  const int seg = blockIdx.x, b = seg / (int)per, sr = seg % (int)per, hk = sr / a.groups, r = blockIdx.y;
+  const int row = sr % a.groups * kRows + r;
+  if (row >= a.rows) return;
+  const size_t qrow = ((size_t)b * c.H + (size_t)hk * c.group) * a.T + row;
+  const int nb = l.cum[b + 1] - l.cum[b];
+  const unsigned lo = (unsigned)l.cum[b] * per + (unsigned)sr * nb, hi = lo + nb;
+  const unsigned c0 = nb ? lo / run : 0, c1 = nb ? (hi - 1) / run : 0;
+  if (nb != 0 && c0 == c1) return;  // written by the CTA that had all of it
+  float m = -INFINITY, sum = 0.f, o[E];
+  for (int e = 0; e < E; ++e) o[e] = 0.f;
+  if (nb != 0) {
+    for (unsigned i = c0 + lane; i <= c1; i += 32) m = fmaxf(m, a.part_ml[((size_t)i + seg) * 2 * kRows + r]);
+    for (int s = 16; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
+    const float top = m == -INFINITY ? 0.f : m;
+#pragma unroll 4
+    for (unsigned i = c0 + warp; i <= c1; i += kWarps) {
+      const size_t part = (size_t)i + seg;
+      const float f = tc::ex2_approx(a.part_ml[part * 2 * kRows + r] - top);
+      sum += a.part_ml[part * 2 * kRows + kRows + r] * f;
+      const float* p = a.part_o + (part * kRows + r) * D + lane * E;
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] += p[e] * f;
+    }
+  }
+  if (lane == 0) s_l[warp] = sum;
+#pragma unroll
   for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = o[e];
   __syncthreads();
-  float top = -INFINITY, sum = 0.f;
-  for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w]);
-  for (int w = 0; w < kWarps; ++w) sum += s_l[w] == 0.f ? 0.f : s_l[w] * __expf(s_m[w] - top);  // 0: no slot; NaN stays
-  if (threadIdx.x < D) {
+  sum = 0.f;
+  for (int w = 0; w < kWarps; ++w) sum += s_l[w];
+  const bool valid = row % a.T < l.fresh[b] && sum != 0.f;
+  if (tid < D) {
     float y = 0.f;
-    for (int w = 0; w < kWarps; ++w)
-      if (s_l[w] != 0.f) y += s_o[w][threadIdx.x] * __expf(s_m[w] - top);
-    a.out[row * D + threadIdx.x] = __float2bfloat16(sum == 0.f ? 0.f : y / sum);
+    for (int w = 0; w < kWarps; ++w) y += s_o[w][tid];
+    a.out[qrow * D + tid] = __float2bfloat16(valid ? y / sum : 0.f);
   }
-  if (threadIdx.x == 0) a.lse[row] = sum == 0.f ? -INFINITY : top + logf(sum);
+  if (tid == 0 && a.lse != nullptr) a.lse[qrow] = log2_sum(m, sum);
 }
 
-// weight[b, hk, s] += sum over the group's heads and the step's rows of exp(score - lse).
-// One CTA a (block, sequence, KV head); a warp a slot.
-template <int KIND, int D>
+// ---------------------------------------------------------------------------
+// weights: weight[b, hk, s] += sum over rows of 2^(score - lse), rows in order
+// ---------------------------------------------------------------------------
+// A warp a tile (list entries that name no block are passed over), a lane two slots.
 __global__ void __launch_bounds__(kThreads) weight_kernel(const CacheView c, const Step a) {
-  constexpr int E = D / 32;
-  const int j = blockIdx.x, b = blockIdx.y / c.H_kv, hk = blockIdx.y % c.H_kv;
+  extern __shared__ char raw[];
+  __shared__ int warp_sums[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  bool bad = false;
-  const int L = checked_len(a.lens, b, c.cap, &bad), n = checked_new(a.n_new, b, a.T, &bad);
-  if (j * kBlock >= L) return;
-  const int page = checked_page(c, b, j);
-  if (page < 0) return;
-  const size_t ph = (size_t)page * c.H_kv + hk;
-  const bool chosen = a.sel ? in_list(a.sel + ((size_t)b * c.H_kv + hk) * a.top_n, a.top_n, j) : a.window == 0;
-  for (int r = warp; r < kBlock && j * kBlock + r < L; r += kWarps) {
-    const int s = j * kBlock + r;
-    float sum = 0.f;
+  Lines l;
+  scan_lines(c, a, raw, &l, warp_sums);
+  const unsigned per = c.H_kv, total = (unsigned)l.cum[c.B] * per;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  for (unsigned t = blockIdx.x * kWarps + warp; t < total; t += gridDim.x * kWarps) {
+    const int b = find_sequence(l, c.B, t, per), nb = l.cum[b + 1] - l.cum[b], L = l.len[b], n = l.fresh[b];
+    const unsigned in = t - (unsigned)l.cum[b] * per;
+    const int hk = (int)(in / (unsigned)nb);
+    bool chosen;
+    const int j = tile_block(c, a, b, hk, (int)(in - (unsigned)hk * nb), L, n, lane, &chosen);
+    if (j < 0) continue;
+    const int page = c.table[(size_t)b * c.max_blocks + j];
+    if (page < 0 || page >= c.n_pages) continue;  // reported by the attention kernel
+    const size_t qrow0 = ((size_t)b * c.H + (size_t)hk * c.group) * a.T;
+    const float2* s = reinterpret_cast<const float2*>(a.scores + (size_t)t * a.rows * kBlock) + lane;
+    const float* lse = a.lse + qrow0;
+    float x = 0.f, y = 0.f;
     for (int g = 0; g < c.group; ++g)
-      for (int t = 0; t < n; ++t) {
-        const int pos = L - n + t;
-        if (s > pos || !(chosen || s > pos - a.window)) continue;
-        const size_t row = ((size_t)b * c.H + hk * c.group + g) * a.T + t;
-        float q[E];
-        for (int e = 0; e < E; ++e) q[e] = __bfloat162float(a.q[row * D + lane * E + e]);
-        sum += __expf(score_of<KIND, D>(c, ph, r, q, lane) - a.lse[row]);
+#pragma unroll 4
+      for (int i = 0; i < n; ++i) {
+        const int r = g * a.T + i;
+        const float2 v = s[r * (kBlock / 2)];
+        const float z = lse[r];
+        if (z != -INFINITY) {
+          x += tc::ex2_approx(v.x - z);
+          y += tc::ex2_approx(v.y - z);
+        }
       }
-    if (lane == 0) c.weight[((size_t)b * c.H_kv + hk) * c.cap + s] += sum;
+    const int slot = j * kBlock + 2 * lane;
+    float* w = c.weight + ((size_t)b * c.H_kv + hk) * c.cap + slot;
+    if (slot + 1 < L) {
+      float2* w2 = reinterpret_cast<float2*>(w);
+      float2 v = *w2;
+      v.x += x;
+      v.y += y;
+      *w2 = v;
+    } else if (slot < L) {
+      *w += x;
+    }
   }
 }
 
-sla_status check_step(const sla_cache_config* c, int32_t T, int32_t top_n, int32_t window) {
+// ---------------------------------------------------------------------------
+// host
+// ---------------------------------------------------------------------------
+int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return 0;
+  return n;
+}
+
+constexpr int kMaxCtas = 2 * 148;  // a workspace is sized for this grid, whatever device is current
+
+struct Layout {
+  size_t ml, o, lse, scores, total;
+  int rows, groups;
+};
+
+// Most tiles that a (sequence, KV head) can have.
+int most_tiles(const sla_cache_config* c, int T, int top_n, int window) {
+  const int64_t range = window > 0 ? ((int64_t)window + T - 2) / kBlock + 2 : c->max_blocks;
+  const int blocks = (int)(range < c->max_blocks ? range : c->max_blocks);
+  return top_n > 0 ? top_n + (window > 0 ? blocks : 0) : blocks;
+}
+
+sla_status plan_step(const sla_cache_config* c, int32_t T, int32_t top_n, int32_t window, bool weights, Layout* p) {
   const sla_status st = sla_cache_validate_config(c);
   if (st != SLA_OK) return st;
   if (T < 1 || top_n < 0 || window < 0) return SLA_ERR_INVALID_ARG;
-  if (T > kCacheMaxT || (int64_t)T * (c->H / c->H_kv) > kCacheMaxRows || top_n > kCacheMaxSel)
-    return SLA_ERR_UNSUPPORTED;
+  const int64_t rows = (int64_t)T * (c->H / c->H_kv);
+  if (T > kCacheMaxT || rows > kCacheMaxRows || top_n > kCacheMaxSel) return SLA_ERR_UNSUPPORTED;
+  p->rows = (int)rows;
+  p->groups = (p->rows + kRows - 1) / kRows;
+  const int64_t segs = (int64_t)c->B * c->H_kv * p->groups;
+  const int64_t tiles = (int64_t)c->B * c->H_kv * most_tiles(c, T, top_n, window);
+  if (tiles * p->groups >= ((int64_t)1 << 31)) return SLA_ERR_UNSUPPORTED;  // the line is counted in 32 bits
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = off;
+    off = align_up(off + bytes, 256);
+    return o;
+  };
+  const size_t parts = kMaxCtas + (size_t)segs;
+  p->ml = take(parts * 2 * kRows * 4);
+  p->o = take(parts * kRows * c->d * 4);
+  p->lse = take(weights ? (size_t)c->B * c->H * T * 4 : 0);
+  p->scores = take(weights ? (size_t)tiles * p->rows * kBlock * 4 : 0);
+  p->total = off;
   return SLA_OK;
+}
+
+cudaError_t launch_after(cudaLaunchConfig_t* cfg, dim3 grid, size_t smem, cudaStream_t s, cudaLaunchAttribute* at) {
+  *cfg = cudaLaunchConfig_t{};
+  cfg->gridDim = grid;
+  cfg->blockDim = dim3(kThreads);
+  cfg->dynamicSmemBytes = smem;
+  cfg->stream = s;
+  at->id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at->val.programmaticStreamSerializationAllowed = 1;
+  cfg->attrs = at;
+  cfg->numAttrs = 1;
+  return cudaSuccess;
+}
+
+template <int KIND, int D>
+cudaError_t launch(const CacheView& c, const Step& a, int sms, cudaStream_t s) {
+  CUtensorMap kmap, vmap;
+  const uint64_t rows = (uint64_t)c.n_pages * c.H_kv * kBlock;
+  if (!make_tmap_rows_u8(&kmap, c.k, rows, D, kBlock) || !make_tmap_rows_u8(&vmap, c.v, rows, D, kBlock))
+    return cudaErrorInvalidValue;
+  auto attend = attend_kernel<KIND, D>;
+  cudaError_t e = cudaFuncSetAttribute(attend, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Smem<D>::bytes(kCacheMaxB));
+  if (e != cudaSuccess) return e;
+  const int ctas = 2 * sms < kMaxCtas ? 2 * sms : kMaxCtas;
+  attend<<<ctas, kThreads, Smem<D>::bytes(c.B), s>>>(kmap, vmap, c, a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute at[1];
+  const int segs = c.B * c.H_kv * a.groups;
+  launch_after(&cfg, dim3(segs, a.rows < kRows ? a.rows : kRows), lines_bytes(c.B), s, at);
+  e = cudaLaunchKernelEx(&cfg, join_kernel<D>, c, a, (unsigned)ctas);
+  if (e != cudaSuccess || c.weight == nullptr) return e;
+  launch_after(&cfg, dim3(8 * sms), lines_bytes(c.B), s, at);
+  return cudaLaunchKernelEx(&cfg, weight_kernel, c, a);
 }
 
 }  // namespace
@@ -146,8 +795,8 @@ extern "C" {
 
 size_t sla_cache_attend_workspace_bytes(const sla_cache_config* cfg, int32_t T, int32_t top_n, int32_t window,
                                         int32_t with_weight) {
-  if (check_step(cfg, T, top_n, window) != SLA_OK) return 0;
-  return align_up((size_t)cfg->B * cfg->H * T * sizeof(float), 256);
+  Layout p;
+  return plan_step(cfg, T, top_n, window, with_weight != 0, &p) == SLA_OK ? p.total : 0;
 }
 
 sla_status sla_cache_attend(const void* q, const sla_cache_config* cfg, const sla_cache* cache, int32_t T,
@@ -156,38 +805,38 @@ sla_status sla_cache_attend(const void* q, const sla_cache_config* cfg, const sl
   CacheView c;
   sla_status st = check_cache(cfg, cache, &c);
   if (st != SLA_OK) return st;
-  st = check_step(cfg, T, top_n, window);
+  Layout p;
+  st = plan_step(cfg, T, top_n, window, c.weight != nullptr, &p);
   if (st != SLA_OK) return st;
   if (!q || !lens || !out || q == out || (sel == nullptr) != (top_n == 0)) return SLA_ERR_INVALID_ARG;
   if (((uintptr_t)q % 16) || ((uintptr_t)out % 16) || ((uintptr_t)lens % 4) || ((uintptr_t)n_new % 4) ||
       ((uintptr_t)sel % 4))
     return SLA_ERR_INVALID_ARG;
-  if (!ws || ((uintptr_t)ws % 256) ||
-      ws_bytes < sla_cache_attend_workspace_bytes(cfg, T, top_n, window, c.weight != nullptr))
-    return SLA_ERR_WORKSPACE;
+  if (!ws || ((uintptr_t)ws % 256) || ws_bytes < p.total) return SLA_ERR_WORKSPACE;
   Step a;
   a.q = (const __nv_bfloat16*)q;
   a.lens = lens;
   a.n_new = n_new;
   a.sel = sel;
   a.out = (__nv_bfloat16*)out;
-  a.lse = (float*)ws;
+  a.part_ml = (float*)((char*)ws + p.ml);
+  a.part_o = (float*)((char*)ws + p.o);
+  a.lse = c.weight ? (float*)((char*)ws + p.lse) : nullptr;
+  a.scores = c.weight ? (float*)((char*)ws + p.scores) : nullptr;
   a.T = T;
   a.top_n = top_n;
-  a.window = window;
+  a.window = window < c.cap + kCacheMaxT ? window : c.cap + kCacheMaxT;  // more sees no more
+  a.rows = p.rows;
+  a.groups = p.groups;
+  const int sms = sm_count();
+  if (sms < 1) return SLA_ERR_CUDA;
   cudaStream_t s = (cudaStream_t)stream;
-  auto run = [&](auto attend, auto weigh) {
-    attend<<<dim3(c.B * c.H, T), kThreads, 0, s>>>(c, a);
-    if (c.weight != nullptr) weigh<<<dim3(c.max_blocks, c.B * c.H_kv), kThreads, 0, s>>>(c, a);
-  };
-  if (c.kind == SLA_CACHE_E4M3) {
-    if (c.d == 128) run(attend_kernel<SLA_CACHE_E4M3, 128>, weight_kernel<SLA_CACHE_E4M3, 128>);
-    else run(attend_kernel<SLA_CACHE_E4M3, 64>, weight_kernel<SLA_CACHE_E4M3, 64>);
-  } else {
-    if (c.d == 128) run(attend_kernel<SLA_CACHE_INT8, 128>, weight_kernel<SLA_CACHE_INT8, 128>);
-    else run(attend_kernel<SLA_CACHE_INT8, 64>, weight_kernel<SLA_CACHE_INT8, 64>);
-  }
-  return cudaGetLastError() == cudaSuccess ? SLA_OK : SLA_ERR_CUDA;
+  cudaError_t e;
+  if (c.kind == SLA_CACHE_E4M3)
+    e = c.d == 128 ? launch<SLA_CACHE_E4M3, 128>(c, a, sms, s) : launch<SLA_CACHE_E4M3, 64>(c, a, sms, s);
+  else
+    e = c.d == 128 ? launch<SLA_CACHE_INT8, 128>(c, a, sms, s) : launch<SLA_CACHE_INT8, 64>(c, a, sms, s);
+  return e == cudaSuccess ? SLA_OK : SLA_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -79,6 +79,10 @@ struct Args {
 bool make_tmap_3d(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
                   uint64_t s1, uint64_t s2, uint32_t b0, uint32_t b1);
 
+// 2D byte map [rows][d] of the 8-bit cache (d 64 or 128), boxes of box_rows whole rows, with
+// the swizzle of a row's length (64 or 128 bytes).
+bool make_tmap_rows_u8(CUtensorMap* map, const void* base, uint64_t rows, int d, uint32_t box_rows);
+
 // kernel launchers (return the launch error)
 cudaError_t launch_pool(const Plan& p, const Args& a, cudaStream_t s);
 cudaError_t launch_kcos(const Plan& p, const Args& a, cudaStream_t s);  // cos_filter flags

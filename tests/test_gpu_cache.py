@@ -708,7 +708,8 @@ def test_python_refusals():
     p = Pair(B=2, H=4, H_kv=2, d=64)
     p.fill([10, 20])
     q, lens = p.queries(1), i32(p.lens)
-    out, ws = torch.empty_like(q), torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+    out = torch.empty_like(q)
+    ws = torch.empty(sla.sla_cache_attend_workspace_bytes(p.cfg, 1, 0, 0, True), dtype=torch.uint8, device="cuda")
 
     def attend(q=q, cfg=p.cfg, cache=p.c, lens=lens, n_new=None, sel=None, window=0, out=out, ws=ws):
         sla.sla_cache_attend(q, cfg, cache, lens, n_new, sel, window, out, ws)
