@@ -5,6 +5,7 @@
 #include <math.h>
 
 #include "cache.cuh"
+#include "tc.cuh"
 
 namespace sla {
 
@@ -56,18 +57,20 @@ sla_status check_cache(const sla_cache_config* c, const sla_cache* m, CacheView*
 
 namespace {
 
-// Largest of one non-negative value a thread over the block's 256 threads (all get it).
-__device__ __forceinline__ float block_max_256(float a, uint32_t* slots) {
-  const uint32_t w = __reduce_max_sync(0xffffffffu, __float_as_uint(a));
+constexpr int kCta = 256;
+
+// Largest of one unsigned value a thread over the block (all get it). slots: 8 words.
+__device__ __forceinline__ uint32_t block_max(uint32_t a, uint32_t* slots) {
+  const uint32_t w = __reduce_max_sync(0xffffffffu, a);
   if ((threadIdx.x & 31) == 0) slots[threadIdx.x >> 5] = w;
   __syncthreads();
   uint32_t m = slots[0];
 #pragma unroll
-  for (int i = 1; i < 8; ++i) m = max(m, slots[i]);
-  return __uint_as_float(m);
+  for (int i = 1; i < kCta / 32; ++i) m = max(m, slots[i]);
+  return m;
 }
 
-// One 16-element chunk of a row as its 16 code bytes.
+// Sixteen codes of 16 values times inv.
 template <int KIND>
 __device__ __forceinline__ uint4 encode16(const float* x, float inv) {
   uint4 c;
@@ -77,45 +80,66 @@ __device__ __forceinline__ uint4 encode16(const float* x, float inv) {
   c.w = encode4<KIND>(x[12] * inv, x[13] * inv, x[14] * inv, x[15] * inv);
   return c;
 }
+// Codes at a scale `ratio` times as fine (a power of two): rounded again, exact for ratio >= 1.
 template <int KIND>
-__device__ __forceinline__ void decode16(const uint4& c, float* x) {
-  decode4<KIND>(c.x, x);
-  decode4<KIND>(c.y, x + 4);
-  decode4<KIND>(c.z, x + 8);
-  decode4<KIND>(c.w, x + 12);
+__device__ __forceinline__ uint4 recode16(const uint4& c, float ratio) {
+  float y[16];
+  decode4<KIND>(c.x, y);
+  decode4<KIND>(c.y, y + 4);
+  decode4<KIND>(c.z, y + 8);
+  decode4<KIND>(c.w, y + 12);
+  return encode16<KIND>(y, ratio);
 }
 
-// Mean over 64 rows of codes in shared memory, times the scale. Codes are integers times
-// 2^-9 (e4m3) or integers (int8) of at most 19 bits, so 64 of them add up exactly in fp32.
+// Mean of a page's 64 rows of codes in shared memory, times the scale. Codes are integers
+// times 2^-9 (e4m3) or integers (int8) of at most 19 bits, so 64 of them add up exactly in
+// fp32, in any order. All threads; parts: kCta * 4 floats.
 template <int KIND, int D>
-__device__ __forceinline__ void write_mean(const uint8_t* tile, float scale, float* mean) {
-  for (int c = threadIdx.x; c < D / 4; c += blockDim.x) {
-    float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
-    for (int r = 0; r < kBlock; ++r) {
-      float x[4];
-      decode4<KIND>(reinterpret_cast<const uint32_t*>(tile + r * D)[c], x);
-      s0 += x[0];
-      s1 += x[1];
-      s2 += x[2];
-      s3 += x[3];
+__device__ __forceinline__ void write_mean(const uint8_t* tile, float scale, float* mean, float4* parts) {
+  constexpr int W = D / 4, P = kCta / W, R = kBlock / P;  // words a row, threads a word, rows a thread
+  const int w = threadIdx.x % W, p = threadIdx.x / W;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    float x[4];
+    decode4<KIND>(reinterpret_cast<const uint32_t*>(tile + (p * R + r) * D)[w], x);
+    s.x += x[0];
+    s.y += x[1];
+    s.z += x[2];
+    s.w += x[3];
+  }
+  parts[threadIdx.x] = s;
+  __syncthreads();
+  if (threadIdx.x < W) {
+#pragma unroll
+    for (int i = 1; i < P; ++i) {
+      const float4 y = parts[i * W + threadIdx.x];
+      s.x += y.x;
+      s.y += y.y;
+      s.z += y.z;
+      s.w += y.w;
     }
     const float f = scale * (1.f / kBlock);
-    reinterpret_cast<float4*>(mean)[c] = make_float4(s0 * f, s1 * f, s2 * f, s3 * f);
+    reinterpret_cast<float4*>(mean)[threadIdx.x] = make_float4(s.x * f, s.y * f, s.z * f, s.w * f);
   }
 }
 
 // ---------------------------------------------------------------------------
-// append: one CTA a (block that may be written, KV head, sequence), keys and values apart
+// append: one CTA a (block that may be written, KV head, sequence), keys and values apart.
+// A thread holds its 16-element chunks as the bf16 words that it loaded (8 registers) and
+// takes the largest magnitude on their bits, which order like the magnitudes.
 // ---------------------------------------------------------------------------
 template <int KIND, int D>
-__global__ void __launch_bounds__(256) append_kernel(const CacheView c, const __nv_bfloat16* __restrict__ k_new,
-                                                     const __nv_bfloat16* __restrict__ v_new, int T,
-                                                     const int32_t* __restrict__ lens,
-                                                     const int32_t* __restrict__ n_new, int32_t* lens_out) {
-  constexpr int C = D / 16;            // chunks of 16 elements a row
-  constexpr int NT = kBlock * C / 256;  // chunks a thread
-  __shared__ uint32_t slots[8];
+__global__ void __launch_bounds__(kCta) append_kernel(const CacheView c, const __nv_bfloat16* __restrict__ k_new,
+                                                      const __nv_bfloat16* __restrict__ v_new, int T,
+                                                      const int32_t* __restrict__ lens,
+                                                      const int32_t* __restrict__ n_new, int32_t* lens_out) {
+  constexpr int C = D / 16;             // chunks of 16 elements a row
+  constexpr int NT = kBlock * C / kCta;  // chunks a thread
+  constexpr uint32_t kTop = 0x7b80;     // 2^120 in bf16
+  __shared__ uint32_t slots[kCta / 32];
   __shared__ __align__(16) uint8_t tile[kBlock * D];
+  __shared__ float4 parts[kCta];
   const int hk = blockIdx.x % c.H_kv, jj = blockIdx.x / c.H_kv, b = blockIdx.y;
   const bool is_k = blockIdx.z == 0;
   const int L = lens[b], n = n_new ? n_new[b] : T;
@@ -129,64 +153,73 @@ __global__ void __launch_bounds__(256) append_kernel(const CacheView c, const __
   if (first >= L + n || n == 0) return;
   const int lo = max(L - first, 0), hi = min(L + n - first, kBlock);  // rows of the page written now
   const int page = checked_page(c, b, j);
+  const __nv_bfloat16* src = (is_k ? k_new : v_new) + ((size_t)b * c.H_kv + hk) * T * D;
+
+  uint32_t x[NT][8];
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    const int task = threadIdx.x + kCta * i, r = task / C, ch = task % C;
+    uint4 u = make_uint4(0u, 0u, 0u, 0u), w = u;
+    if (r >= lo && r < hi) {
+      const uint4* p = reinterpret_cast<const uint4*>(src + (size_t)(first + r - L) * D + ch * 16);
+      u = __ldcs(p);
+      w = __ldcs(p + 1);
+    }
+    x[i][0] = u.x, x[i][1] = u.y, x[i][2] = u.z, x[i][3] = u.w;
+    x[i][4] = w.x, x[i][5] = w.y, x[i][6] = w.z, x[i][7] = w.w;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) top = __vmaxu2(top, x[i][e] & 0x7fff7fffu);
+  }
   if (page < 0) return;
   const size_t ph = (size_t)page * c.H_kv + hk;
   uint8_t* codes = (is_k ? c.k : c.v) + ph * kBlock * D;
   float* scale = (is_k ? c.k_scale : c.v_scale) + ph;
-  const __nv_bfloat16* src = (is_k ? k_new : v_new) + ((size_t)b * c.H_kv + hk) * T * D;
-
-  float x[NT][16];
-  float amax = 0.f;
-  bool odd = false;
+  top = max(top & 0xffffu, top >> 16);
+  if (top > kTop) {  // NaN becomes 0, larger magnitudes 2^120
+    report(c.status, SLA_ERR_DEVICE_CHECK, kDetailCacheValue);
+    top = 0;
 #pragma unroll
-  for (int i = 0; i < NT; ++i) {
-    const int task = threadIdx.x + 256 * i, r = task / C, ch = task % C;
-    if (r >= lo && r < hi) {
-      const uint4* p = reinterpret_cast<const uint4*>(src + (size_t)(first + r - L) * D + ch * 16);
-      const uint4 u = p[0], w = p[1];
-      const uint32_t words[8] = {u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w};
+    for (int i = 0; i < NT; ++i)
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float2 f = unpack_bf16(words[e]);
-        x[i][2 * e] = f.x;
-        x[i][2 * e + 1] = f.y;
-      }
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        if (!(fabsf(x[i][e]) <= kCacheMaxAbs)) {
-          odd = true;
-          x[i][e] = isnan(x[i][e]) ? 0.f : copysignf(kCacheMaxAbs, x[i][e]);
+        uint32_t y = 0;
+        for (int s = 0; s < 32; s += 16) {
+          uint32_t h = (x[i][e] >> s) & 0xffffu, mag = h & 0x7fffu;
+          mag = mag > 0x7f80u ? 0u : min(mag, kTop);
+          top = max(top, mag);
+          y |= ((h & 0x8000u) | mag) << s;
         }
-        amax = fmaxf(amax, fabsf(x[i][e]));
+        x[i][e] = y;
       }
-    }
   }
-  if (odd) report(c.status, SLA_ERR_DEVICE_CHECK, kDetailCacheValue);
   const bool open = lo > 0;
   const float was = open ? *scale : 0.f;
-  amax = block_max_256(amax, slots);  // every thread has read the old scale behind this barrier
-  const float to = fmaxf(was, exp2_int(scale_exponent<KIND>(amax)));
+  top = block_max(top, slots);  // every thread has read the old scale behind this barrier
+  const float to = fmaxf(was, exp2_int(scale_exponent<KIND>(__uint_as_float(top << 16))));
   const float inv = 1.f / to;
   const bool again = open && to != was;  // the codes held are rounded at the new scale
   const bool full = hi == kBlock && is_k && c.k_mean != nullptr;
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
-    const int task = threadIdx.x + 256 * i, r = task / C, ch = task % C;
+    const int task = threadIdx.x + kCta * i, r = task / C, ch = task % C;
     uint4* at = reinterpret_cast<uint4*>(codes + r * D + ch * 16);
     uint4 code = make_uint4(0u, 0u, 0u, 0u);
-    if (r >= lo && r < hi) {
-      code = encode16<KIND>(x[i], inv);
+    if (r >= lo) {  // slots behind the last token hold 0
+      float y[16];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        y[2 * e] = __uint_as_float(x[i][e] << 16);
+        y[2 * e + 1] = __uint_as_float(x[i][e] & 0xffff0000u);
+      }
+      code = encode16<KIND>(y, inv);
       *at = code;
-    } else if (r < lo) {
+    } else {
       if (again || full) code = *at;
       if (again) {
-        float y[16];
-        decode16<KIND>(code, y);
-        code = encode16<KIND>(y, was * inv);
+        code = recode16<KIND>(code, was * inv);
         *at = code;
       }
-    } else {
-      *at = code;  // slots behind the last token hold 0
     }
     if (full) *reinterpret_cast<uint4*>(tile + r * D + ch * 16) = code;
   }
@@ -195,98 +228,175 @@ __global__ void __launch_bounds__(256) append_kernel(const CacheView c, const __
     c.weight[((size_t)b * c.H_kv + hk) * c.cap + first + threadIdx.x] = 0.f;
   if (full) {
     __syncthreads();
-    write_mean<KIND, D>(tile, to, c.k_mean + ph * D);
+    write_mean<KIND, D>(tile, to, c.k_mean + ph * D, parts);
   }
 }
 
 // ---------------------------------------------------------------------------
-// evict, first step: which slots stay (one CTA a sequence and KV head)
+// evict, first step: which slots stay (one cluster of eight CTAs a sequence and KV head)
 //
 // The budget - n_sink - n_recent heaviest of the slots between are those above a threshold
-// weight and the first few equal to it. The threshold is found digit by digit (8 bits of
-// the weight's order-preserving integer at a time, a histogram each), then every warp
-// counts its run of slots and, after a scan over the warps, writes its kept slots in order.
+// weight and the first few equal to it. Each CTA keeps its eighth of the weights in shared
+// memory as integers of the same order. The threshold is found digit by digit, 8 bits at a
+// time: the CTAs' histograms are added through distributed shared memory. Weights crowd in
+// a few digits, so lanes with the same digit count together before the shared atomic. Then
+// every CTA counts its run, takes its place from the counts of those before, and writes its
+// kept slots in order.
 // ---------------------------------------------------------------------------
+constexpr int kSelCluster = 8;
+constexpr int kSelThreads = 1024;
+
 __device__ __forceinline__ uint32_t weight_key(float w) {
   if (isnan(w)) w = -INFINITY;
   const uint32_t u = __float_as_uint(w + 0.f);  // -0 counts as 0
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The word at the same place of another CTA's shared memory.
+__device__ __forceinline__ int peer_int(const int* p, uint32_t rank) {
+  uint32_t addr;
+  int v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
 
-__global__ void __launch_bounds__(1024) evict_select_kernel(const CacheView c, const int32_t* __restrict__ lens,
-                                                            int budget, int n_sink, int n_recent,
-                                                            int32_t* __restrict__ kept, int32_t* lens_out) {
-  __shared__ int hist[256];
+// Slots of one CTA's run: a multiple of 32 a warp.
+__host__ __device__ inline int select_run(int n) {
+  return (int)align_up((size_t)(n + kSelCluster - 1) / kSelCluster, kSelThreads);
+}
+
+__global__ void __cluster_dims__(kSelCluster, 1, 1) __launch_bounds__(kSelThreads)
+    evict_select_kernel(const CacheView c, const int32_t* __restrict__ lens, int budget, int n_sink, int n_recent,
+                        int32_t* __restrict__ kept, int32_t* lens_out, int* __restrict__ flags, int n_flags) {
+  extern __shared__ uint32_t keys[];  // [select_run(cap)]
+  __shared__ int hist[2][256], total[256];
   __shared__ int s_digit, s_rest;
-  __shared__ int above[32], equal[32];
-  const int b = blockIdx.x / c.H_kv, hk = blockIdx.x % c.H_kv;
+  __shared__ int above[32], equal[32], mine[2];
+  const int bh = blockIdx.x / kSelCluster, b = bh / c.H_kv, hk = bh % c.H_kv;
+  const int rank = (int)cluster_rank();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  asm volatile("griddepcontrol.launch_dependents;");
   bool bad = false;
   const int n = checked_len(lens, b, c.cap, &bad), m = min(n, budget);
-  if (hk == 0 && tid == 0) {
+  if (hk == 0 && rank == 0 && tid == 0) {
     if (bad) report(c.status, SLA_ERR_DEVICE_CHECK, kDetailCacheLen);
     lens_out[b] = m;
   }
-  int32_t* out = kept + (size_t)blockIdx.x * budget;
-  for (int i = m + tid; i < budget; i += 1024) out[i] = -1;
-  if (n <= budget) {
-    for (int i = tid; i < n; i += 1024) out[i] = i;
+  // what the move's CTAs of this sequence and head count and signal with
+  for (int i = rank * kSelThreads + tid; i < n_flags; i += kSelCluster * kSelThreads) flags[(size_t)bh * n_flags + i] = 0;
+  int32_t* out = kept + (size_t)bh * budget;
+  for (int i = m + rank * kSelThreads + tid; i < budget; i += kSelCluster * kSelThreads) out[i] = -1;
+  if (n <= budget) {  // the same for the whole cluster
+    for (int i = rank * kSelThreads + tid; i < n; i += kSelCluster * kSelThreads) out[i] = i;
     return;
   }
-  const float* w = c.weight + (size_t)blockIdx.x * c.cap;
-  const int lo = n_sink, hi = n - n_recent;  // n_sink + n_recent <= budget < n: lo < hi
-  int rest = budget - n_sink - n_recent;     // still to be taken among the keys that match the prefix
+  const float* w = c.weight + (size_t)bh * c.cap;
+  const int run = select_run(n), a = min(n, rank * run), z = min(n, a + run);
+  const int lo = n_sink, hi = n - n_recent;    // n_sink + n_recent <= budget < n: lo < hi
+  const int want = budget - n_sink - n_recent;  // of the slots between
+  for (int i = a + tid; i < z; i += kSelThreads) keys[i - a] = weight_key(w[i]);
+  if (tid < 256) hist[0][tid] = hist[1][tid] = 0;
+  __syncthreads();
+  int rest = want;  // still to be taken among the keys that match the prefix
   uint32_t prefix = 0;
-  if (rest > 0) {
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      if (tid < 256) hist[tid] = 0;
-      __syncthreads();
+  if (want > 0) {
+    int turn = 0;
+    for (int shift = 24; shift >= 0; shift -= 8, turn ^= 1) {
       const uint32_t mask = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
-      for (int i = lo + tid; i < hi; i += 1024) {
-        const uint32_t key = weight_key(w[i]);
-        if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & 255u], 1);
+      for (int i = a + tid; i - lane < z; i += kSelThreads) {
+        uint32_t dig = 256;
+        if (i < z && i >= lo && i < hi && (keys[i - a] & mask) == prefix) dig = (keys[i - a] >> shift) & 255u;
+        const uint32_t same = __match_any_sync(0xffffffffu, dig);
+        if (dig < 256 && lane == __ffs(same) - 1) atomicAdd(&hist[turn][dig], __popc(same));
+      }
+      cluster_sync();
+      if (tid < 256) {
+        int s = 0;
+#pragma unroll
+        for (int r = 0; r < kSelCluster; ++r) s += peer_int(&hist[turn][tid], r);
+        total[tid] = s;
+        hist[turn ^ 1][tid] = 0;  // read by the others before the barrier above, if at all
       }
       __syncthreads();
-      if (tid == 0) {
-        int left = rest, dgt = 255;
-        while (hist[dgt] < left) left -= hist[dgt--];  // at least `rest` keys match: ends at dgt >= 0
-        s_digit = dgt;
-        s_rest = left;
+      if (warp == 0) {  // digit whose keys, from the largest down, hold the rest-th one
+        int v[8], s = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          v[i] = total[255 - 8 * lane - i];
+          s += v[i];
+        }
+        int upto = s;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, upto, o);
+          if (lane >= o) upto += y;
+        }
+        int before = upto - s;
+        if (before < rest && upto >= rest) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            if (before < rest && before + v[i] >= rest) {
+              s_digit = 255 - 8 * lane - i;
+              s_rest = rest - before;
+              before = 1 << 30;
+            } else {
+              before += v[i];
+            }
+          }
+        }
       }
       __syncthreads();
       prefix |= (uint32_t)s_digit << shift;
       rest = s_rest;
     }
   }
-  // keys above prefix stay, and the first `rest` equal to it (none of either where rest was 0)
-  const bool any = budget - n_sink - n_recent > 0;
-  const int per = ((n + 31) / 32 + 31) / 32 * 32, a = min(n, warp * per), z = min(n, a + per);
+  // keys above prefix stay, and the first `rest` equal to it (none of either where want is 0)
+  const int per = run / 32, wa = min(z, a + warp * per), wz = min(z, wa + per);
   int n_above = 0, n_equal = 0;
-  for (int i = a + lane; i - lane < z; i += 32) {
-    const bool in = i < z && i >= lo && i < hi;
-    const bool held = i < z && (i < lo || i >= hi);
-    const uint32_t key = in ? weight_key(w[i]) : 0u;
-    n_above += __popc(__ballot_sync(0xffffffffu, held || (in && any && key > prefix)));
-    n_equal += __popc(__ballot_sync(0xffffffffu, in && any && key == prefix));
+  for (int i = wa + lane; i - lane < wz; i += 32) {
+    const bool held = i < wz && (i < lo || i >= hi), in = i < wz && !held && want > 0;
+    const uint32_t key = in ? keys[i - a] : 0u;
+    n_above += __popc(__ballot_sync(0xffffffffu, held || (in && key > prefix)));
+    n_equal += __popc(__ballot_sync(0xffffffffu, in && key == prefix));
   }
   if (lane == 0) {
     above[warp] = n_above;
     equal[warp] = n_equal;
   }
   __syncthreads();
+  if (warp == 0) {
+    const int x = __reduce_add_sync(0xffffffffu, above[lane]), y = __reduce_add_sync(0xffffffffu, equal[lane]);
+    if (lane == 0) {
+      mine[0] = x;
+      mine[1] = y;
+    }
+  }
+  cluster_sync();
   int at = 0, eq = 0;
+  for (int r = 0; r < rank; ++r) {
+    at += peer_int(&mine[0], r);
+    eq += peer_int(&mine[1], r);
+  }
+  cluster_sync();  // no CTA leaves while another reads its counts
   for (int i = 0; i < warp; ++i) {
     at += above[i];
     eq += equal[i];
   }
   at += min(eq, rest);
-  for (int i = a + lane; i - lane < z; i += 32) {
-    const bool in = i < z && i >= lo && i < hi;
-    const bool held = i < z && (i < lo || i >= hi);
-    const uint32_t key = in ? weight_key(w[i]) : 0u;
+  for (int i = wa + lane; i - lane < wz; i += 32) {
+    const bool held = i < wz && (i < lo || i >= hi), in = i < wz && !held && want > 0;
+    const uint32_t key = in ? keys[i - a] : 0u;
     const uint32_t below = (1u << lane) - 1u;
-    const uint32_t eqs = __ballot_sync(0xffffffffu, in && any && key == prefix);
-    const bool take = held || (in && any && (key > prefix || (key == prefix && eq + __popc(eqs & below) < rest)));
+    const uint32_t eqs = __ballot_sync(0xffffffffu, in && key == prefix);
+    const bool take = held || (in && (key > prefix || (key == prefix && eq + __popc(eqs & below) < rest)));
     const uint32_t takes = __ballot_sync(0xffffffffu, take);
     if (take) out[at + __popc(takes & below)] = i;
     at += __popc(takes);
@@ -295,80 +405,149 @@ __global__ void __launch_bounds__(1024) evict_select_kernel(const CacheView c, c
 }
 
 // ---------------------------------------------------------------------------
-// evict, second step: the kept slots move (one CTA a sequence and KV head, keys and values
-// apart, new blocks in ascending order: kept[i] >= i, so a new block's page, where it is
-// the old one of that place, holds no slot that a later new block reads)
+// evict, second step: the kept slots move, one CTA a (new block, KV head, sequence)
+//
+// A CTA loads its 64 rows of keys and values (16-byte chunks of whole rows, as codes), takes
+// the largest magnitudes, and writes the block. Where the new page is the old one of that
+// place it still holds rows that other new blocks load: those that keep slots of old block
+// j are one or two (kept is ascending and kept[i] >= i), all of them at or before j. So every
+// CTA signals when its loads are done, and one that writes in place first waits for those
+// few. CTAs take their block from a counter of their sequence and head when they start: one
+// that waits has only such before it that have started, and none of them waits before it has
+// signalled.
 // ---------------------------------------------------------------------------
+// first i in [0, m) with from[i] >= slot, m if none
+__device__ __forceinline__ int first_kept(const int32_t* from, int m, int slot) {
+  int lo = 0, hi = m;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (from[mid] < slot) lo = mid + 1;
+    else hi = mid;
+  }
+  return lo;
+}
+
 template <int KIND, int D>
-__global__ void __launch_bounds__(256) evict_move_kernel(const CacheView c, const int32_t* __restrict__ kept,
-                                                         const int32_t* __restrict__ lens, int budget,
-                                                         const int32_t* __restrict__ dst_table, float* weight_out) {
+__global__ void __launch_bounds__(kCta) evict_move_kernel(const CacheView c, const int32_t* kept,
+                                                          const int32_t* lens, int budget, const int32_t* dst_table,
+                                                          float* weight_out, int* flags, int n_flags) {
   constexpr int C = D / 16;
-  constexpr int NT = kBlock * C / 256;
-  __shared__ uint32_t slots[8];
+  constexpr int NT = kBlock * C / kCta;
+  __shared__ uint32_t slots[2][kCta / 32];
   __shared__ __align__(16) uint8_t tile[kBlock * D];
-  const int b = blockIdx.x / c.H_kv, hk = blockIdx.x % c.H_kv;
-  const bool is_k = blockIdx.z == 0;
+  __shared__ float4 parts[kCta];
+  __shared__ int s_slot[kBlock], s_ph[kBlock];
+  __shared__ int s_j, s_late;
+  const int tid = threadIdx.x, nd = (budget + kBlock - 1) / kBlock;
+  const int bh = blockIdx.x / nd, b = bh / c.H_kv, hk = bh % c.H_kv;
   bool bad = false;
   const int m = min(checked_len(lens, b, c.cap, &bad), budget);
-  const int nd = (budget + kBlock - 1) / kBlock;
-  const int32_t* from = kept + (size_t)blockIdx.x * budget;
-  const size_t wrow = (size_t)blockIdx.x * c.cap;
-  uint8_t* pool = is_k ? c.k : c.v;
-  float* scales = is_k ? c.k_scale : c.v_scale;
-  for (int j = 0; j * kBlock < m; ++j) {
-    float x[NT][16];
-    float amax = 0.f, w = 0.f;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  int* done = flags + (size_t)bh * n_flags;  // [nd] signals, then the counter
+  if (tid == 0) {
+    s_j = atomicAdd(&done[nd], 1);
+    s_late = 0;
+  }
+  __syncthreads();
+  const int j = s_j, first = j * kBlock;
+  if (first >= m) return;
+  const int32_t* from = kept + (size_t)bh * budget;
+  if (tid < kBlock) {
+    const int slot = first + tid < m ? from[first + tid] : -1;
+    const int page = slot < 0 ? -1 : checked_page(c, b, slot / kBlock);
+    s_slot[tid] = slot;
+    s_ph[tid] = page < 0 ? -1 : page * c.H_kv + hk;
+  }
+  const int to_page = dst_table[(size_t)b * nd + j];
+  const bool in_place = to_page == c.table[(size_t)b * c.max_blocks + j];
+  __syncthreads();
+  uint4 kc[NT], vc[NT];
+  float ks[NT], vs[NT];
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      const int task = threadIdx.x + 256 * i, r = task / C, ch = task % C;
-      const int slot = j * kBlock + r < m ? from[j * kBlock + r] : -1;
-      const int page = slot < 0 ? -1 : checked_page(c, b, slot / kBlock);
+  for (int i = 0; i < NT; ++i) {
+    const int task = tid + kCta * i, r = task / C, ch = task % C, ph = s_ph[r];
+    kc[i] = vc[i] = make_uint4(0u, 0u, 0u, 0u);
+    ks[i] = vs[i] = 0.f;
+    if (ph >= 0) {
+      const size_t at = ((size_t)ph * kBlock + s_slot[r] % kBlock) * D + ch * 16;
+      kc[i] = *reinterpret_cast<const uint4*>(c.k + at);
+      vc[i] = *reinterpret_cast<const uint4*>(c.v + at);
+      ks[i] = c.k_scale[ph];
+      vs[i] = c.v_scale[ph];
+    }
+  }
+  const size_t wrow = (size_t)bh * c.cap;
+  const float w = tid < kBlock && s_slot[tid] >= 0 ? c.weight[wrow + s_slot[tid]] : 0.f;
+  float ka = 0.f, va = 0.f;
 #pragma unroll
-      for (int e = 0; e < 16; ++e) x[i][e] = 0.f;
-      if (page >= 0) {
-        const size_t ph = (size_t)page * c.H_kv + hk;
-        const uint4 code = *reinterpret_cast<const uint4*>(pool + (ph * kBlock + slot % kBlock) * D + ch * 16);
-        const float s = scales[ph];
-        decode16<KIND>(code, x[i]);
+  for (int i = 0; i < NT; ++i) {
+    float x[4];
+    decode4<KIND>(max_byte(__vmaxu4(__vmaxu4(abs4<KIND>(kc[i].x), abs4<KIND>(kc[i].y)),
+                                    __vmaxu4(abs4<KIND>(kc[i].z), abs4<KIND>(kc[i].w)))), x);
+    ka = fmaxf(ka, fabsf(x[0] * ks[i]));
+    decode4<KIND>(max_byte(__vmaxu4(__vmaxu4(abs4<KIND>(vc[i].x), abs4<KIND>(vc[i].y)),
+                                    __vmaxu4(abs4<KIND>(vc[i].z), abs4<KIND>(vc[i].w)))), x);
+    va = fmaxf(va, fabsf(x[0] * vs[i]));
+  }
+  const uint32_t kw = __reduce_max_sync(0xffffffffu, __float_as_uint(ka));
+  const uint32_t vw = __reduce_max_sync(0xffffffffu, __float_as_uint(va));
+  if ((tid & 31) == 0) {
+    slots[0][tid >> 5] = kw;
+    slots[1][tid >> 5] = vw;
+  }
+  __syncthreads();  // every thread has its rows
+  uint32_t km = slots[0][0], vm = slots[1][0];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          x[i][e] *= s;
-          amax = fmaxf(amax, fabsf(x[i][e]));
+  for (int i = 1; i < kCta / 32; ++i) {
+    km = max(km, slots[0][i]);
+    vm = max(vm, slots[1][i]);
+  }
+  if (tid == 0) {
+    asm volatile("fence.acq_rel.gpu;\n\tst.relaxed.gpu.global.s32 [%0], 1;" ::"l"(done + j) : "memory");
+    if (in_place || weight_out == c.weight) {
+      const int i0 = first_kept(from, m, first), i1 = first_kept(from, m, first + kBlock);
+      const uint64_t t0 = tc::globaltimer();
+      for (int y = i0 / kBlock; y * kBlock < i1 && y < j; ++y) {
+        int seen = 0;
+        for (;;) {
+          asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(seen) : "l"(done + y) : "memory");
+          if (seen || tc::globaltimer() - t0 > tc::kTimeoutNs) break;
+          __nanosleep(50);
         }
+        if (!seen) s_late = 1;
       }
-      if (is_k && ch == 0 && slot >= 0) w = c.weight[wrow + slot];
-      if (is_k && ch == 0) {
-        // held until every thread has read its sources
-        if (slot >= 0) reinterpret_cast<float*>(tile)[r] = w;
-      }
+      if (s_late) report(c.status, SLA_ERR_DEVICE_TIMEOUT, kDetailTimeout);
     }
-    amax = block_max_256(fminf(amax, kCacheMaxAbs), slots);
-    if (is_k && threadIdx.x < kBlock && j * kBlock + threadIdx.x < m)
-      weight_out[wrow + j * kBlock + threadIdx.x] = reinterpret_cast<const float*>(tile)[threadIdx.x];
-    __syncthreads();
-    const int page = dst_table[(size_t)b * nd + j];
-    if (page < 0 || page >= c.n_pages) {
-      if (threadIdx.x == 0) report(c.status, SLA_ERR_DEVICE_CHECK, kDetailCachePage);
-      continue;
-    }
-    const size_t ph = (size_t)page * c.H_kv + hk;
-    const int ex = scale_exponent<KIND>(amax);
-    const float inv = exp2_int(-ex);
-    const bool full = (j + 1) * kBlock <= m && is_k && c.k_mean != nullptr;
+  }
+  __syncthreads();
+  if (s_late) return;  // the old rows stay as they are
+  if (tid < kBlock && first + tid < m) weight_out[wrow + first + tid] = w;
+  if (to_page < 0 || to_page >= c.n_pages) {
+    if (tid == 0) report(c.status, SLA_ERR_DEVICE_CHECK, kDetailCachePage);
+    return;
+  }
+  const size_t ph = (size_t)to_page * c.H_kv + hk;
+  const int ke = scale_exponent<KIND>(fminf(__uint_as_float(km), kCacheMaxAbs));
+  const int ve = scale_exponent<KIND>(fminf(__uint_as_float(vm), kCacheMaxAbs));
+  const float kt = exp2_int(ke), vt = exp2_int(ve);
+  const bool full = first + kBlock <= m && c.k_mean != nullptr;
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      const int task = threadIdx.x + 256 * i, r = task / C, ch = task % C;
-      const uint4 code = encode16<KIND>(x[i], inv);
-      *reinterpret_cast<uint4*>(pool + (ph * kBlock + r) * D + ch * 16) = code;
-      if (full) *reinterpret_cast<uint4*>(tile + r * D + ch * 16) = code;
-    }
-    if (threadIdx.x == 0) scales[ph] = exp2_int(ex);
-    if (full) {
-      __syncthreads();
-      write_mean<KIND, D>(tile, exp2_int(ex), c.k_mean + ph * D);
-    }
+  for (int i = 0; i < NT; ++i) {
+    const int task = tid + kCta * i, r = task / C, ch = task % C;
+    const size_t at = (ph * kBlock + r) * D + ch * 16;
+    if (ks[i] != kt) kc[i] = recode16<KIND>(kc[i], ks[i] * exp2_int(-ke));
+    if (vs[i] != vt) vc[i] = recode16<KIND>(vc[i], vs[i] * exp2_int(-ve));
+    *reinterpret_cast<uint4*>(c.k + at) = kc[i];
+    *reinterpret_cast<uint4*>(c.v + at) = vc[i];
+    if (full) *reinterpret_cast<uint4*>(tile + r * D + ch * 16) = kc[i];
+  }
+  if (tid == 0) {
+    c.k_scale[ph] = kt;
+    c.v_scale[ph] = vt;
+  }
+  if (full) {
     __syncthreads();
+    write_mean<KIND, D>(tile, kt, c.k_mean + ph * D, parts);
   }
 }
 
@@ -407,9 +586,12 @@ sla_status sla_cache_append(const void* k, const void* v, const sla_cache_config
   return cudaGetLastError() == cudaSuccess ? SLA_OK : SLA_ERR_CUDA;
 }
 
+// ints a (sequence, KV head): a signal of each new block, a counter
+static int evict_flags(int budget) { return (budget + kBlock - 1) / kBlock + 1; }
+
 size_t sla_cache_evict_workspace_bytes(const sla_cache_config* cfg, int32_t budget) {
   if (check_sizes(cfg) != SLA_OK || budget < 1 || budget > cfg->max_blocks * kBlock) return 0;
-  return 256;
+  return align_up((size_t)cfg->B * cfg->H_kv * evict_flags(budget) * sizeof(int), 256);
 }
 
 sla_status sla_cache_evict(const sla_cache_config* cfg, const sla_cache* cache, const int32_t* lens, int32_t budget,
@@ -425,20 +607,38 @@ sla_status sla_cache_evict(const sla_cache_config* cfg, const sla_cache* cache, 
     return SLA_ERR_INVALID_ARG;
   if (budget < 1 || budget > c.cap || n_sink < 0 || n_recent < 0 || n_sink > budget - n_recent)
     return SLA_ERR_INVALID_ARG;
+  if ((int64_t)c.B * c.H_kv * (evict_flags(budget) - 1) >= ((int64_t)1 << 31)) return SLA_ERR_UNSUPPORTED;  // grid
   if (!ws || !aligned_to(ws, 256) || ws_bytes < sla_cache_evict_workspace_bytes(cfg, budget))
     return SLA_ERR_WORKSPACE;
   cudaStream_t s = (cudaStream_t)stream;
-  evict_select_kernel<<<c.B * c.H_kv, 1024, 0, s>>>(c, lens, budget, n_sink, n_recent, kept, lens_out);
-  const dim3 grid((unsigned)(c.B * c.H_kv), 1, 2);
-  auto run = [&](auto kernel) { kernel<<<grid, 256, 0, s>>>(c, kept, lens, budget, dst_table, weight_out); };
-  if (c.kind == SLA_CACHE_E4M3) {
-    if (c.d == 128) run(evict_move_kernel<SLA_CACHE_E4M3, 128>);
-    else run(evict_move_kernel<SLA_CACHE_E4M3, 64>);
-  } else {
-    if (c.d == 128) run(evict_move_kernel<SLA_CACHE_INT8, 128>);
-    else run(evict_move_kernel<SLA_CACHE_INT8, 64>);
-  }
-  return cudaGetLastError() == cudaSuccess ? SLA_OK : SLA_ERR_CUDA;
+  int* flags = (int*)ws;
+  const int n_flags = evict_flags(budget), nd = n_flags - 1;
+  const int smem = select_run(c.cap) * (int)sizeof(uint32_t);
+  if (cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           select_run(kMaxBlocks * kBlock) * (int)sizeof(uint32_t)) != cudaSuccess)
+    return SLA_ERR_CUDA;
+  evict_select_kernel<<<c.B * c.H_kv * kSelCluster, kSelThreads, smem, s>>>(c, lens, budget, n_sink, n_recent, kept,
+                                                                           lens_out, flags, n_flags);
+  if (cudaGetLastError() != cudaSuccess) return SLA_ERR_CUDA;
+  cudaLaunchConfig_t launch = {};
+  launch.gridDim = dim3((unsigned)(c.B * c.H_kv * nd));
+  launch.blockDim = dim3(kCta);
+  launch.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  launch.attrs = at;
+  launch.numAttrs = 1;
+  auto run = [&](auto kernel) {
+    return cudaLaunchKernelEx(&launch, kernel, c, (const int32_t*)kept, lens, (int)budget, dst_table, weight_out, flags,
+                              n_flags);
+  };
+  cudaError_t e;
+  if (c.kind == SLA_CACHE_E4M3)
+    e = c.d == 128 ? run(evict_move_kernel<SLA_CACHE_E4M3, 128>) : run(evict_move_kernel<SLA_CACHE_E4M3, 64>);
+  else
+    e = c.d == 128 ? run(evict_move_kernel<SLA_CACHE_INT8, 128>) : run(evict_move_kernel<SLA_CACHE_INT8, 64>);
+  return e == cudaSuccess ? SLA_OK : SLA_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -51,9 +51,11 @@ __device__ __forceinline__ uint32_t encode4(float x0, float x1, float x2, float 
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(x3), "f"(x2));
     return (uint32_t)lo | ((uint32_t)hi << 16);
   }
-  const uint32_t a = (uint32_t)__float2int_rn(x0) & 255u, b = (uint32_t)__float2int_rn(x1) & 255u;
-  const uint32_t c = (uint32_t)__float2int_rn(x2) & 255u, e = (uint32_t)__float2int_rn(x3) & 255u;
-  return a | (b << 8) | (c << 16) | (e << 24);
+  // |x| <= 128: adding 1.5 * 2^23 rounds to an integer (ties to even) in the low mantissa bits
+  const float big = 12582912.f;
+  const uint32_t a = __float_as_uint(x0 + big), b = __float_as_uint(x1 + big);
+  const uint32_t c = __float_as_uint(x2 + big), e = __float_as_uint(x3 + big);
+  return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, e, 0x0040), 0x5410);
 }
 
 // two codes (the low 16 bits of c) as fp16, exactly: |e4m3| <= 448 and its subnormals are
@@ -70,6 +72,16 @@ __device__ __forceinline__ uint32_t decode2_f16(uint32_t c) {
   const __half2 bias = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
   const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&w), bias);
   return *reinterpret_cast<const uint32_t*>(&y);
+}
+
+// largest code magnitude of four codes, as a code byte; e4m3 magnitudes order like integers
+template <int KIND>
+__device__ __forceinline__ uint32_t abs4(uint32_t c) {
+  return KIND == SLA_CACHE_E4M3 ? c & 0x7f7f7f7fu : __vabsss4(c);
+}
+__device__ __forceinline__ uint32_t max_byte(uint32_t c) {
+  c = __vmaxu4(c, c >> 16);
+  return max(c & 255u, (c >> 8) & 255u);
 }
 
 template <int KIND>
