@@ -371,17 +371,29 @@ def _cache_cfg(c) -> sla_cache_config:
     return c if isinstance(c, sla_cache_config) else make_cache_config(c)
 
 
-def _typed(x, name: str, shape, dtypes, device):
+torch = None  # loaded with the first SlaCache, which every call below needs
+_BF16 = _F32 = _I32 = ()
+
+
+def _load_torch() -> None:
+    global torch, _BF16, _F32, _I32
+    if torch is None:
+        import torch as module
+        torch = module
+        _BF16, _F32, _I32 = (torch.bfloat16,), (torch.float32,), (torch.int32,)
+
+
+def _typed(x, name: str, shape, dtypes, index: int):
     """x's address, after checking what the kernels take for granted of it."""
     if x is None:
         return None
-    if tuple(x.shape) != tuple(shape):
-        raise ValueError(f"{name}: shape {tuple(x.shape)}, expected {tuple(shape)}")
-    if x.dtype not in dtypes:
-        raise ValueError(f"{name}: dtype {x.dtype}, expected {' or '.join(map(str, dtypes))}")
-    if x.device != device:
-        raise ValueError(f"{name}: on {x.device}, the cache is on {device}")
-    if not x.is_contiguous():
+    if x.shape != shape or x.dtype not in dtypes or x.get_device() != index or not x.is_contiguous():
+        if tuple(x.shape) != tuple(shape):
+            raise ValueError(f"{name}: shape {tuple(x.shape)}, expected {tuple(shape)}")
+        if x.dtype not in dtypes:
+            raise ValueError(f"{name}: dtype {x.dtype}, expected {' or '.join(map(str, dtypes))}")
+        if x.get_device() != index:
+            raise ValueError(f"{name}: on {x.device}, the cache is on cuda:{index}")
         raise ValueError(f"{name}: must be contiguous")
     return x.data_ptr()
 
@@ -399,19 +411,19 @@ class SlaCache:
     status        int32 [64], zeroed once (sla_check_device_status(cache.status) reads it)
     """
 
-    __slots__ = ("k", "v", "k_scale", "v_scale", "k_mean", "weight", "block_table", "status", "device", "kind",
-                 "shape", "_c")
+    __slots__ = ("k", "v", "k_scale", "v_scale", "k_mean", "weight", "block_table", "status", "device", "index",
+                 "kind", "shape", "_c")
 
     def __init__(self, k, v, k_scale, v_scale, k_mean, weight, block_table, status):
-        import torch
+        _load_torch()
         if not k.is_cuda:
             raise ValueError("tensor must live on a CUDA device")
         if k.dim() != 4 or block_table.dim() != 2:
             raise ValueError("k: 4 dimensions expected, block_table: 2")
         n_pages, H_kv, block, d = k.shape
         B, max_blocks = block_table.shape
-        bytes_, f32, i32 = (torch.uint8, torch.int8, torch.float8_e4m3fn), (torch.float32,), (torch.int32,)
-        dev = k.device
+        bytes_, f32, i32 = (torch.uint8, torch.int8, torch.float8_e4m3fn), _F32, _I32
+        dev = k.get_device()
         c = sla_cache()
         c.k = _typed(k, "k", (n_pages, H_kv, 64, d), bytes_, dev)
         c.v = _typed(v, "v", (n_pages, H_kv, 64, d), bytes_, dev)
@@ -423,7 +435,8 @@ class SlaCache:
         c.status = _typed(status, "status", (64,), i32, dev)
         self.k, self.v, self.k_scale, self.v_scale, self.k_mean = k, v, k_scale, v_scale, k_mean
         self.weight, self.block_table, self.status = weight, block_table, status
-        self.device, self._c = dev, c
+        self.device, self._c = k.device, c
+        self.index = dev
         # the element type where the dtype names one (uint8 holds either)
         self.kind = {torch.int8: SLA_CACHE_INT8, torch.float8_e4m3fn: SLA_CACHE_E4M3}.get(k.dtype)
         if v.dtype != k.dtype:
@@ -433,7 +446,7 @@ class SlaCache:
     @classmethod
     def empty(cls, c, device="cuda", weight: bool = True, k_mean: bool = True) -> "SlaCache":
         """A zeroed cache for c whose block table has no page yet (-1 everywhere)."""
-        import torch
+        _load_torch()
         dt = torch.float8_e4m3fn if c.kind == SLA_CACHE_E4M3 else torch.int8
 
         def zeros(*shape, dtype=torch.float32):
@@ -451,21 +464,27 @@ class SlaCache:
 def _cache_call(c, cache: SlaCache) -> sla_cache_config:
     """The configuration, after checking that it describes the cache and that the cache's
     device is the current one (the library launches on the current device)."""
-    import torch
-    cfg = _cache_cfg(c)
+    cfg = c if isinstance(c, sla_cache_config) else make_cache_config(c)
     if (cfg.B, cfg.H_kv, cfg.d, cfg.n_pages, cfg.max_blocks) != cache.shape:
         raise ValueError(f"the configuration's (B, H_kv, d, n_pages, max_blocks) "
                          f"{(cfg.B, cfg.H_kv, cfg.d, cfg.n_pages, cfg.max_blocks)} are not the cache's {cache.shape}")
     if cache.kind is not None and cache.kind != cfg.kind:
         raise ValueError("the configuration's kind is not the cache's dtype")
-    if cache.device.index != torch.cuda.current_device():
+    if cache.index != torch.cuda.current_device():
         raise ValueError(f"the cache is on {cache.device}, the current device is cuda:{torch.cuda.current_device()}")
     return cfg
 
 
-def _ws_args(ws, device):
-    if ws.device != device:
-        raise ValueError(f"ws: on {ws.device}, the cache is on {device}")
+def _cache_stream(stream, cache: SlaCache) -> int:
+    """The given stream's handle, or the current one's without building a Stream object."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(cache.index)
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _ws_args(ws, cache: SlaCache):
+    if ws.get_device() != cache.index:
+        raise ValueError(f"ws: on {ws.device}, the cache is on {cache.device}")
     return _ptr(ws), ws.numel() * ws.element_size()
 
 
@@ -475,28 +494,26 @@ def sla_cache_validate_config(c) -> int:
 
 def sla_cache_append(k, v, c, cache: SlaCache, lens, n_new=None, lens_out=None, stream=None) -> None:
     """Writes the first n_new[b] rows of k, v (bf16 [B, H_kv, T, d]) behind lens[b] cached tokens."""
-    import torch
     cfg = _cache_call(c, cache)
-    dev, bf16, i32 = cache.device, (torch.bfloat16,), (torch.int32,)
+    dev, bf16, i32 = cache.index, _BF16, _I32
     T = k.shape[2] if k.dim() == 4 else -1
     _check(lib().sla_cache_append(
         _typed(k, "k", (cfg.B, cfg.H_kv, T, cfg.d), bf16, dev), _typed(v, "v", (cfg.B, cfg.H_kv, T, cfg.d), bf16, dev),
         ctypes.byref(cfg), ctypes.byref(cache._c), T, _typed(lens, "lens", (cfg.B,), i32, dev),
         _typed(n_new, "n_new", (cfg.B,), i32, dev), _typed(lens_out, "lens_out", (cfg.B,), i32, dev),
-        _stream(stream)), "sla_cache_append")
+        _cache_stream(stream, cache)), "sla_cache_append")
 
 
 def sla_cache_route(q, c, cache: SlaCache, lens, n_new, sel, stream=None) -> None:
     """The top_n = sel.shape[2] past blocks of a step's queries q (bf16 [B, H, T, d])."""
-    import torch
     cfg = _cache_call(c, cache)
-    dev, i32 = cache.device, (torch.int32,)
+    dev, i32 = cache.index, _I32
     T = q.shape[2] if q.dim() == 4 else -1
     top_n = sel.shape[2] if sel.dim() == 3 else -1
     _check(lib().sla_cache_route(
-        _typed(q, "q", (cfg.B, cfg.H, T, cfg.d), (torch.bfloat16,), dev), ctypes.byref(cfg), ctypes.byref(cache._c),
+        _typed(q, "q", (cfg.B, cfg.H, T, cfg.d), _BF16, dev), ctypes.byref(cfg), ctypes.byref(cache._c),
         T, _typed(lens, "lens", (cfg.B,), i32, dev), _typed(n_new, "n_new", (cfg.B,), i32, dev), top_n,
-        _typed(sel, "sel", (cfg.B, cfg.H_kv, top_n), i32, dev), _stream(stream)), "sla_cache_route")
+        _typed(sel, "sel", (cfg.B, cfg.H_kv, top_n), i32, dev), _cache_stream(stream, cache)), "sla_cache_route")
 
 
 def sla_cache_attend_workspace_bytes(c, T: int, top_n: int = 0, window: int = 0, with_weight: bool = False) -> int:
@@ -507,17 +524,16 @@ def sla_cache_attend_workspace_bytes(c, T: int, top_n: int = 0, window: int = 0,
 def sla_cache_attend(q, c, cache: SlaCache, lens, n_new, sel, window, out, ws, stream=None) -> None:
     """Attention of a step's queries q (bf16 [B, H, T, d]) over the cache: all of it (sel None,
     window 0), the last `window` tokens (sel None), or the blocks in sel and the window."""
-    import torch
     cfg = _cache_call(c, cache)
-    dev, bf16, i32 = cache.device, (torch.bfloat16,), (torch.int32,)
+    dev, bf16, i32 = cache.index, _BF16, _I32
     T = q.shape[2] if q.dim() == 4 else -1
     top_n = 0 if sel is None else sel.shape[2] if sel.dim() == 3 else -1
-    ws_ptr, ws_bytes = _ws_args(ws, dev)
+    ws_ptr, ws_bytes = _ws_args(ws, cache)
     _check(lib().sla_cache_attend(
         _typed(q, "q", (cfg.B, cfg.H, T, cfg.d), bf16, dev), ctypes.byref(cfg), ctypes.byref(cache._c), T,
         _typed(lens, "lens", (cfg.B,), i32, dev), _typed(n_new, "n_new", (cfg.B,), i32, dev),
         _typed(sel, "sel", (cfg.B, cfg.H_kv, top_n), i32, dev), top_n, int(window),
-        _typed(out, "out", (cfg.B, cfg.H, T, cfg.d), bf16, dev), ws_ptr, ws_bytes, _stream(stream)), "sla_cache_attend")
+        _typed(out, "out", (cfg.B, cfg.H, T, cfg.d), bf16, dev), ws_ptr, ws_bytes, _cache_stream(stream, cache)), "sla_cache_attend")
 
 
 def sla_cache_evict_workspace_bytes(c, budget: int) -> int:
@@ -528,16 +544,15 @@ def sla_cache_evict(c, cache: SlaCache, lens, budget, n_sink, n_recent, dst_tabl
                     stream=None) -> None:
     """Cuts every sequence to `budget` tokens, those of largest cache.weight; dst_table (int32
     [B, ceil(budget / 64)]) names the pages that receive them (the cache's own or new ones)."""
-    import torch
     cfg = _cache_call(c, cache)
-    dev, i32 = cache.device, (torch.int32,)
-    ws_ptr, ws_bytes = _ws_args(ws, dev)
+    dev, i32 = cache.index, _I32
+    ws_ptr, ws_bytes = _ws_args(ws, cache)
     _check(lib().sla_cache_evict(
         ctypes.byref(cfg), ctypes.byref(cache._c), _typed(lens, "lens", (cfg.B,), i32, dev), int(budget), int(n_sink),
         int(n_recent), _typed(dst_table, "dst_table", (cfg.B, -(-budget // 64)), i32, dev),
-        _typed(weight_out, "weight_out", (cfg.B, cfg.H_kv, 64 * cfg.max_blocks), (torch.float32,), dev),
+        _typed(weight_out, "weight_out", (cfg.B, cfg.H_kv, 64 * cfg.max_blocks), _F32, dev),
         _typed(kept, "kept", (cfg.B, cfg.H_kv, budget), i32, dev), _typed(lens_out, "lens_out", (cfg.B,), i32, dev),
-        ws_ptr, ws_bytes, _stream(stream)), "sla_cache_evict")
+        ws_ptr, ws_bytes, _cache_stream(stream, cache)), "sla_cache_evict")
 
 
 def sla_version() -> str:
