@@ -58,20 +58,24 @@ __device__ __forceinline__ uint32_t encode4(float x0, float x1, float x2, float 
   return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, e, 0x0040), 0x5410);
 }
 
-// two codes (the low 16 bits of c) as fp16, exactly: |e4m3| <= 448 and its subnormals are
+// four codes as fp16 pairs (lo: bytes 0 and 1), exactly: |e4m3| <= 448 and its subnormals are
 // fp16 normals or subnormals; |int8| <= 128
 template <int KIND>
-__device__ __forceinline__ uint32_t decode2_f16(uint32_t c) {
+__device__ __forceinline__ void decode4_f16(uint32_t c, uint32_t& lo, uint32_t& hi) {
   if (KIND == SLA_CACHE_E4M3) {
-    uint32_t r;
-    asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(c));
-    return r;
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(c));
+    return;
   }
   // byte ^ 0x80 = code + 128 in the mantissa of 1024 + (code + 128); minus 1152
-  const uint32_t w = __byte_perm(c ^ 0x8080u, 0x64646464u, 0x4140);
+  const uint32_t u = c ^ 0x80808080u, a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
   const __half2 bias = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
-  const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&w), bias);
-  return *reinterpret_cast<const uint32_t*>(&y);
+  const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&a), bias);
+  const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&b), bias);
+  lo = *reinterpret_cast<const uint32_t*>(&x);
+  hi = *reinterpret_cast<const uint32_t*>(&y);
 }
 
 // largest code magnitude of four codes, as a code byte; e4m3 magnitudes order like integers
@@ -86,7 +90,8 @@ __device__ __forceinline__ uint32_t max_byte(uint32_t c) {
 
 template <int KIND>
 __device__ __forceinline__ void decode4(uint32_t c, float* x) {
-  const uint32_t a = decode2_f16<KIND>(c & 0xffffu), b = decode2_f16<KIND>(c >> 16);
+  uint32_t a, b;
+  decode4_f16<KIND>(c, a, b);
   const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&a));
   const float2 g = __half22float2(*reinterpret_cast<const __half2*>(&b));
   x[0] = f.x;

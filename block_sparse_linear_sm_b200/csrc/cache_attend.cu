@@ -11,16 +11,19 @@
 // the warps' (max, sum, output) are merged through shared memory and either written out
 // (the CTA had the whole segment) or left as a partial that join_kernel adds up.
 //
-// A warp's tile, by mma.sync m16n8k16 on fp16 (codes are fp16 numbers exactly):
-//   S[16 rows x 64 slots] = Q K^T, k_scale and the softmax scale applied in fp32;
-//   m' = max(m, rowmax S), P = 2^(S - m' + 15) as fp16, l = l 2^(m - m') + 2^-15 sum P;
-//   O = O 2^(m - m') + 2^-15 v_scale * (P V).
+// A warp's tile, by mma.sync m16n8k16 on fp16 (codes are fp16 numbers exactly), with the
+// cache as the 16-row operand and the query rows as the 8 columns, so that up to 8 rows cost
+// half of what 16 do:
+//   S^T[64 slots x rows] = K Q^T; the scales of page, row and softmax in fp32;
+//   m' = max(m, colmax S^T), P = 2^(S - m' + 15) as fp16, l = l 2^(m - m') + 2^-15 sum P;
+//   O^T[d x rows] = O^T 2^(m - m') + 2^-15 v_scale * (V^T P^T).
 // The 15 keeps P's smallest terms out of fp16's subnormals: a weight of 2^-29 still has 11
 // bits. Q is scaled by a power of two a row so that its largest element is in [2^14, 2^15):
 // bf16 elements down to 2^-28 of it are then fp16 numbers exactly.
-// K's product runs over a permuted d (a lane's 16-byte loads of a key row are its k indices
-// of consecutive steps), V's over permuted slots (the order in which ldmatrix hands out the
-// transposed bytes), with Q's and S's columns permuted alike.
+// K Q^T runs over a permuted d (a lane's 16-byte loads of a key row are its k indices of
+// consecutive steps) with Q permuted alike. V^T comes from ldmatrix's transpose of bytes,
+// which hands slots out in another order; the rows of S^T take their keys in that order, and
+// movmatrix turns P's 8 x 8 pieces into the second product's operand.
 #include <cuda.h>
 
 #include "cache.cuh"
@@ -31,7 +34,6 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kRows = 16;       // query rows of a segment
 constexpr int kSlots = 2;       // pages in a warp's ring
 constexpr int kInfo = 4;        // described tiles ahead (at most kSlots + 1 are in use)
 constexpr int kMinRun = kWarps;  // tiles a CTA takes at least
@@ -41,11 +43,12 @@ struct Step {
   const __nv_bfloat16* q;
   const int32_t *lens, *n_new, *sel;
   __nv_bfloat16* out;
-  float* part_ml;   // [slots][2][16]: m, l of a partial
-  float* part_o;    // [slots][16][D]
+  float* part_ml;   // [slots][2][rows of a group]: m, l of a partial
+  float* part_o;    // [slots][rows of a group][D]
   float* lse;       // [B, H, T] log2-sum-exp (with weights)
-  float* scores;    // [tiles of all (sequence, KV head)][rows][64] (with weights)
-  int T, top_n, window, rows, groups;  // rows = T * group of a KV head, in groups of kRows
+  float* scores;    // [tiles of all (sequence, KV head)][64][score_rows] (with weights)
+  int T, top_n, window, rows, groups;  // rows = T * group of a KV head, in groups of 8 or 16
+  int score_rows;                      // rows rounded up to 8
 };
 
 // ---------------------------------------------------------------------------
@@ -172,6 +175,14 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t x) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(addr), "r"(x) : "memory");
+}
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
@@ -271,22 +282,26 @@ __device__ __forceinline__ void pump(Ring<D>& r, const CacheView& c, const Step&
 // ---------------------------------------------------------------------------
 // the attention kernel
 // ---------------------------------------------------------------------------
-template <int D>
+template <int D, int NR>
 struct Smem {
+  static constexpr int kPitch = D + 4;  // words of a merged row: lanes of a store hit all banks
   static constexpr int kRing = kWarps * kSlots * kBlock * D;
-  static constexpr int kMerge = kWarps * kRows * D * 4;
+  static constexpr int kMerge = kWarps * 8 * NR * kPitch * 4;
   static constexpr int off_merge = kRing, off_misc = kRing + kMerge;
   static constexpr int kMisc = 2048;
   static constexpr int off_lines = off_misc + kMisc;
   static size_t bytes(int B) { return off_lines + lines_bytes(B) + 1024; }
 };
 
-template <int KIND, int D>
+// NR: query rows of a segment in eights.
+template <int KIND, int D, int NR>
 __global__ void __launch_bounds__(kThreads, 2)
     attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const CacheView c,
                   const Step a) {
-  constexpr int KS = D / 16;  // k steps of Q K^T; words of codes a lane holds of a key row
-  constexpr int NT = D / 8;   // output column tiles
+  constexpr int KS = D / 16;  // k steps of K Q^T; words of codes a lane holds of a key row
+  constexpr int MT = D / 16;  // row tiles of O^T
+  constexpr int kRows = 8 * NR;
+  using Sm = Smem<D, NR>;
   extern __shared__ char raw[];
   char* smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
   struct Misc {
@@ -296,8 +311,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     int warp_sums[kWarps];
     int abort, never;
   };
-  static_assert(sizeof(Misc) <= Smem<D>::kMisc, "misc");
-  Misc& mi = *reinterpret_cast<Misc*>(smem + Smem<D>::off_misc);
+  static_assert(sizeof(Misc) <= Sm::kMisc, "misc");
+  Misc& mi = *reinterpret_cast<Misc*>(smem + Sm::off_misc);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q4 = lane & 3;
 
   if (tid == 0) {
@@ -309,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     tc::prefetch_tensormap(&vmap);
   }
   Lines l;
-  scan_lines(c, a, smem + Smem<D>::off_lines, &l, mi.warp_sums);
+  scan_lines(c, a, smem + Sm::off_lines, &l, mi.warp_sums);
   asm volatile("griddepcontrol.launch_dependents;");
 
   // this CTA's run of the line
@@ -327,13 +342,12 @@ __global__ void __launch_bounds__(kThreads, 2)
   ring.end = hi;
   ring.seq = find_sequence(l, c.B, lo, per);
   ring.vrow = -1;
+  int b = ring.seq;
   pump(ring, c, a, l, &kmap, &vmap, lane);
 
-  float* merge = reinterpret_cast<float*>(smem + Smem<D>::off_merge);
+  float* merge = reinterpret_cast<float*>(smem + Sm::off_merge);
   bool dead = false;
   unsigned at = lo;  // first tile of the segment being worked on
-  int b = ring.seq;
-  b = find_sequence(l, c.B, lo, per);
   while (at < hi) {
     while ((unsigned)l.cum[b + 1] * per <= at) ++b;
     const int nb = l.cum[b + 1] - l.cum[b], L = l.len[b], n = l.fresh[b];
@@ -343,12 +357,13 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int row0 = grp * kRows;
     const size_t qrow0 = ((size_t)b * c.H + (size_t)hk * c.group) * a.T;
 
-    // Q: two rows of this lane, row g and g + 8, d = q4 * D / 4 ..
-    uint32_t qf[KS][4];
-    float qs[2];
+    // Q^T's columns: this lane holds row g of each eight, d = q4 * D / 4 ..
+    uint32_t qf[NR][KS][2];
+    float qs[NR][2];  // scale of the rows whose scores this lane gets: 8 i + 2 q4 + e
+    int pos[NR][2];   // the slots such a row sees end here
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = row0 + g + 8 * i;
+    for (int i = 0; i < NR; ++i) {
+      const int r = row0 + 8 * i + g;
       float x[D / 4];
 #pragma unroll
       for (int e = 0; e < D / 4; ++e) x[e] = 0.f;
@@ -372,25 +387,28 @@ __global__ void __launch_bounds__(kThreads, 2)
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
       const int ex = max((int)(__float_as_uint(top) >> 23) - 127, -100);
-      const float up = exp2_int(14 - ex);
-      qs[i] = exp2_int(ex - 14) * (c.scale * 1.4426950408889634f);
+      const float up = exp2_int(14 - ex), down = exp2_int(ex - 14) * (c.scale * 1.4426950408889634f);
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
-        qf[s][i] = pack_f16(x[4 * s] * up, x[4 * s + 1] * up);
-        qf[s][i + 2] = pack_f16(x[4 * s + 2] * up, x[4 * s + 3] * up);
+        qf[i][s][0] = pack_f16(x[4 * s] * up, x[4 * s + 1] * up);
+        qf[i][s][1] = pack_f16(x[4 * s + 2] * up, x[4 * s + 3] * up);
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int col = 2 * q4 + e, rc = row0 + 8 * i + col, t = rc % a.T;
+        qs[i][e] = __shfl_sync(0xffffffffu, down, 4 * col);
+        pos[i][e] = rc < a.rows && t < n ? L - n + t : -1;
       }
     }
-    // the slots a row sees end at pos
-    int pos[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = row0 + g + 8 * i, t = r % a.T;
-      pos[i] = r < a.rows && t < n ? L - n + t : -1;
-    }
 
-    float o[NT][4], m[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
+    float o[MT][NR][4], m[NR][2], sum[NR][2];
 #pragma unroll
-    for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    for (int i = 0; i < NR; ++i) {
+      m[i][0] = m[i][1] = -INFINITY;
+      sum[i][0] = sum[i][1] = 0.f;
+#pragma unroll
+      for (int t = 0; t < MT; ++t) o[t][i][0] = o[t][i][1] = o[t][i][2] = o[t][i][3] = 0.f;
+    }
 
     while (ring.used < ring.issued) {
       const TileInfo* ti = &ring.info[(ring.used / 2) % kInfo];
@@ -402,171 +420,206 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (!dead && !tc::mbar_wait(ring.bars + 8 * slot_k, (ring.used / kSlots) & 1, &mi.abort)) dead = true;
       const uint32_t kbase = ring.data + slot_k * Ring<D>::kPage;
 
-      // scores: column 2 q4 + e of tile 2 t + h is slot 16 t + 4 q4 + 2 h + e
-      float s[8][4];
+      // scores: row g (+ 8) of tile t is slot 16 t + 4 (g / 2) + g % 2 (+ 2)
+      float s[4][NR][4];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
+      for (int t = 0; t < 4; ++t)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float(&acc)[4] = s[2 * t + h];
-          acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
-          const int row = 16 * t + 4 * (g >> 1) + (g & 1) + 2 * h;
-          uint32_t w[KS];
+        for (int i = 0; i < NR; ++i) s[t][i][0] = s[t][i][1] = s[t][i][2] = s[t][i][3] = 0.f;
+#pragma unroll
+      for (int u = 0; u < D / 64; ++u)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const int row = 16 * t + 4 * (g >> 1) + (g & 1);
+          uint4 x, y;
           if (D == 128) {
-            const uint32_t at0 = kbase + row * 128;
-            const uint4 x = lds128(at0 + (((2 * q4) ^ (row & 7)) << 4)), y = lds128(at0 + (((2 * q4 + 1) ^ (row & 7)) << 4));
-            w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
-            w[KS - 4] = y.x, w[KS - 3] = y.y, w[KS - 2] = y.z, w[KS - 1] = y.w;
+            x = lds128(kbase + row * 128 + (((2 * q4 + u) ^ (row & 7)) << 4));
+            y = lds128(kbase + (row + 2) * 128 + (((2 * q4 + u) ^ ((row + 2) & 7)) << 4));
           } else {
-            const uint4 x = lds128(kbase + row * 64 + ((q4 ^ ((row >> 1) & 3)) << 4));
-            w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+            x = lds128(kbase + row * 64 + ((q4 ^ ((row >> 1) & 3)) << 4));
+            y = lds128(kbase + (row + 2) * 64 + ((q4 ^ (((row + 2) >> 1) & 3)) << 4));
           }
+          const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-          for (int k = 0; k < KS; ++k)
-            mma_f16(acc, qf[k], decode2_f16<KIND>(w[k] & 0xffffu), decode2_f16<KIND>(w[k] >> 16));
+          for (int k = 0; k < 4; ++k) {
+            uint32_t f[4];
+            decode4_f16<KIND>(xs[k], f[0], f[2]);
+            decode4_f16<KIND>(ys[k], f[1], f[3]);
+#pragma unroll
+            for (int i = 0; i < NR; ++i) mma_f16(s[t][i], f, qf[i][4 * u + k][0], qf[i][4 * u + k][1]);
+          }
         }
-      }
       ++ring.used;
       pump(ring, c, a, l, &kmap, &vmap, lane);
 
-      const float f0 = qs[0] * ks, f1 = qs[1] * ks;
-#pragma unroll
-      for (int t = 0; t < 8; ++t) {
-        s[t][0] *= f0;
-        s[t][1] *= f0;
-        s[t][2] *= f1;
-        s[t][3] *= f1;
-      }
       // rows that do not see the whole page: its end, the window's start
       if (j0 + kBlock - 1 > L - n || (!chosen && j0 <= L - 1 - a.window)) {
 #pragma unroll
-        for (int t = 0; t < 8; ++t)
+        for (int t = 0; t < 4; ++t)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int slot = j0 + 16 * (t >> 1) + 4 * q4 + 2 * (t & 1) + (e & 1), p = pos[e >> 1];
-            if (slot > p || (!chosen && slot <= p - a.window)) s[t][e] = -INFINITY;
-          }
+          for (int i = 0; i < NR; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int slot = j0 + 16 * t + 4 * (g >> 1) + (g & 1) + (e & 2), p = pos[i][e & 1];
+              if (slot > p || (!chosen && slot <= p - a.window)) s[t][i][e] = -INFINITY;
+            }
       }
-      if (a.scores != nullptr) {
+      uint32_t pf[4][NR][2];  // P^T as the second operand of V^T P^T
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int r = row0 + g + 8 * i;
-          if (r < a.rows) {
-            float4* p = reinterpret_cast<float4*>(a.scores + ((size_t)tile * a.rows + r) * kBlock) + q4;
+      for (int i = 0; i < NR; ++i) {
+        // the scale stays positive (a product that underflows would turn a masked score into NaN)
+        const float f[2] = {fmaxf(qs[i][0] * ks, 1e-37f), fmaxf(qs[i][1] * ks, 1e-37f)};
+        // x = (s - tile's maximum) * f + (its scaled value - m') + shift: the largest exponent is
+        // the shift exactly, however large the scores
+        float low[2], off[2], alpha[2];
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
-              p[4 * t] = make_float4(s[2 * t][2 * i], s[2 * t][2 * i + 1], s[2 * t + 1][2 * i], s[2 * t + 1][2 * i + 1]);
-          }
+        for (int e = 0; e < 2; ++e) {
+          float top = fmaxf(s[0][i][e], s[0][i][e + 2]);
+#pragma unroll
+          for (int t = 1; t < 4; ++t) top = tc::fmax3(top, s[t][i][e], s[t][i][e + 2]);
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+          low[e] = top == -INFINITY ? 0.f : top;
+          const float scaled = __fmul_rn(top, f[e]), next = fmaxf(m[i][e], scaled);
+          const float base = next == -INFINITY ? 0.f : next;
+          off[e] = (scaled == -INFINITY ? 0.f : scaled - base) + kShift;
+          alpha[e] = tc::ex2_approx(m[i][e] - base);
+          m[i][e] = next;
+          sum[i][e] *= alpha[e];
         }
-      }
-      float alpha[2], base[2];
+        if (a.scores != nullptr && row0 + 8 * i + 2 * q4 < a.score_rows) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float top = m[i];
+          for (int t = 0; t < 4; ++t)
 #pragma unroll
-        for (int t = 0; t < 8; ++t) top = fmaxf(top, fmaxf(s[t][2 * i], s[t][2 * i + 1]));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        base[i] = top == -INFINITY ? 0.f : top - kShift;
-        alpha[i] = tc::ex2_approx(m[i] - (top == -INFINITY ? 0.f : top));
-        m[i] = top;
-        sum[i] *= alpha[i];
-      }
-      uint32_t pf[4][4];
+            for (int h = 0; h < 2; ++h) {
+              const int slot = 16 * t + 4 * (g >> 1) + (g & 1) + 2 * h;
+              *reinterpret_cast<float2*>(a.scores + ((size_t)tile * kBlock + slot) * a.score_rows + row0 + 8 * i + 2 * q4) =
+                  make_float2(s[t][i][2 * h] * f[0], s[t][i][2 * h + 1] * f[1]);
+            }
+        }
+        const uint64_t f2 = tc::f2_pack(f[0], f[1]), l2 = tc::f2_pack(low[0], low[1]), o2 = tc::f2_pack(off[0], off[1]);
+        uint64_t s2 = tc::f2_pack(sum[i][0], sum[i][1]);
 #pragma unroll
-      for (int t = 0; t < 8; ++t) {
-        float p[4];
+        for (int t = 0; t < 4; ++t) {
+          float p[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) p[e] = tc::ex2_approx(s[t][e] - base[e >> 1]);
-        sum[0] += p[0] + p[1];
-        sum[1] += p[2] + p[3];
-        pf[t >> 1][2 * (t & 1)] = pack_f16(p[0], p[1]);
-        pf[t >> 1][2 * (t & 1) + 1] = pack_f16(p[2], p[3]);
-      }
-      if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+          for (int h = 0; h < 2; ++h) {
+            const uint64_t x = tc::ffma2(tc::fsub2(tc::f2_pack(s[t][i][2 * h], s[t][i][2 * h + 1]), l2), f2, o2);
+            p[2 * h] = tc::ex2_approx(tc::f2_lo(x));
+            p[2 * h + 1] = tc::ex2_approx(tc::f2_hi(x));
+            s2 = tc::fadd2(s2, tc::f2_pack(p[2 * h], p[2 * h + 1]));
+          }
+          pf[t][i][0] = transpose_8x8(pack_f16(p[0], p[1]));
+          pf[t][i][1] = transpose_8x8(pack_f16(p[2], p[3]));
+        }
+        sum[i][0] = tc::f2_lo(s2);
+        sum[i][1] = tc::f2_hi(s2);
+        if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
-          o[i][0] *= alpha[0];
-          o[i][1] *= alpha[0];
-          o[i][2] *= alpha[1];
-          o[i][3] *= alpha[1];
+          for (int t = 0; t < MT; ++t) {
+            o[t][i][0] *= alpha[0];
+            o[t][i][1] *= alpha[1];
+            o[t][i][2] *= alpha[0];
+            o[t][i][3] *= alpha[1];
+          }
         }
       }
 
+      const uint64_t vs2 = tc::f2_pack(vs, vs);
       const uint32_t slot_v = ring.used % kSlots;
       if (!dead && !tc::mbar_wait(ring.bars + 8 * slot_v, (ring.used / kSlots) & 1, &mi.abort)) dead = true;
       const uint32_t vbase = ring.data + slot_v * Ring<D>::kPage;
-      // codes of slots behind the last token are whatever they are: they count as 0
-      uint32_t live[4];
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const int left = L - j0 - 16 * t - 4 * q4;
-        live[t] = left >= 4 ? 0xffffffffu : left <= 0 ? 0u : (1u << (8 * left)) - 1u;
+      if (j0 + kBlock > L) {  // codes of slots behind the last token are whatever they are: they count as 0
+        for (int e = (L - j0) * (D / 16) + lane; e < kBlock * (D / 16); e += 32) sts128(vbase + e * 16, 0u);
+        __syncwarp();
       }
 #pragma unroll
       for (int cc = 0; cc < D / 32; ++cc) {
-        float acc[4][4];
+        float acc[2][NR][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < NR; ++i) acc[h][i][0] = acc[h][i][1] = acc[h][i][2] = acc[h][i][3] = 0.f;
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
           const int row = 16 * t + (lane & 15), ch = 2 * cc + (lane >> 4);
-          const uint32_t addr = vbase + row * D + ((ch ^ (D == 128 ? (row & 7) : ((row >> 1) & 3))) << 4);
           uint32_t w[4];
-          ldmatrix_trans_b8(w, addr);
+          ldmatrix_trans_b8(w, vbase + row * D + ((ch ^ (D == 128 ? (row & 7) : ((row >> 1) & 3))) << 4));
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t x = w[i] & live[t];
-            mma_f16(acc[i], pf[t], decode2_f16<KIND>(x & 0xffffu), decode2_f16<KIND>(x >> 16));
+          for (int h = 0; h < 2; ++h) {
+            uint32_t f[4];
+            decode4_f16<KIND>(w[2 * h], f[0], f[2]);
+            decode4_f16<KIND>(w[2 * h + 1], f[1], f[3]);
+#pragma unroll
+            for (int i = 0; i < NR; ++i) mma_f16(acc[h][i], f, pf[t][i][0], pf[t][i][1]);
           }
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) o[4 * cc + i][e] += vs * acc[i][e];
+          for (int i = 0; i < NR; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; e += 2) {
+              float(&y)[4] = o[2 * cc + h][i];
+              const uint64_t z = tc::ffma2(vs2, tc::f2_pack(acc[h][i][e], acc[h][i][e + 1]), tc::f2_pack(y[e], y[e + 1]));
+              y[e] = tc::f2_lo(z);
+              y[e + 1] = tc::f2_hi(z);
+            }
       }
       ++ring.used;
+      if (j0 + kBlock > L) tc::fence_async_smem();  // the zeros come before the page that is loaded next
       pump(ring, c, a, l, &kmap, &vmap, lane);
     }
 
     // the warps' parts of the segment become one
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 1);
-      sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 2);
-      if (q4 == 0) {
-        mi.m[warp][g + 8 * i] = m[i];
-        mi.l[warp][g + 8 * i] = sum[i] * exp2_int(-(int)kShift);
+    for (int i = 0; i < NR; ++i)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float x = sum[i][e];
+        x += __shfl_xor_sync(0xffffffffu, x, 4);
+        x += __shfl_xor_sync(0xffffffffu, x, 8);
+        x += __shfl_xor_sync(0xffffffffu, x, 16);
+        if (g == 0) {
+          mi.m[warp][8 * i + 2 * q4 + e] = m[i][e];
+          mi.l[warp][8 * i + 2 * q4 + e] = x * exp2_int(-(int)kShift);
+        }
       }
-    }
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = g + 8 * i;
-      float top = mi.m[0][r];
-      for (int w = 1; w < kWarps; ++w) top = fmaxf(top, mi.m[w][r]);
-      const float f = tc::ex2_approx(m[i] - (top == -INFINITY ? 0.f : top));
+    for (int i = 0; i < NR; ++i)
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
-        *reinterpret_cast<float2*>(merge + (warp * kRows + r) * D + 8 * t + 2 * q4) =
-            make_float2(o[t][2 * i] * f, o[t][2 * i + 1] * f);
-    }
+      for (int e = 0; e < 2; ++e) {
+        const int r = 8 * i + 2 * q4 + e;
+        float top = mi.m[0][r];
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) top = fmaxf(top, mi.m[w][r]);
+        const float f = tc::ex2_approx(m[i][e] - (top == -INFINITY ? 0.f : top));
+        float* p = merge + (warp * kRows + r) * Sm::kPitch + g;
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+          p[16 * t] = o[t][i][e] * f;
+          p[16 * t + 8] = o[t][i][e + 2] * f;
+        }
+      }
     __syncthreads();
     const bool whole = seg_lo >= lo && seg_hi <= hi;
     const size_t part = (size_t)blockIdx.x + seg;
     for (int e = tid; e < kRows * D / 4; e += kThreads) {
       const int r = e / (D / 4), d4 = e % (D / 4);
-      float4 y = reinterpret_cast<const float4*>(merge)[e];
+      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+      float top = mi.m[0][r], all = 0.f;
 #pragma unroll
-      for (int w = 1; w < kWarps; ++w) {
-        const float4 x = reinterpret_cast<const float4*>(merge)[w * (kRows * D / 4) + e];
+      for (int w = 0; w < kWarps; ++w) {
+        const float4 x = *reinterpret_cast<const float4*>(merge + (w * kRows + r) * Sm::kPitch + 4 * d4);
         y.x += x.x;
         y.y += x.y;
         y.z += x.z;
         y.w += x.w;
+        top = fmaxf(top, mi.m[w][r]);
       }
-      float top = mi.m[0][r], all = 0.f;
-      for (int w = 1; w < kWarps; ++w) top = fmaxf(top, mi.m[w][r]);
+#pragma unroll
       for (int w = 0; w < kWarps; ++w) all += mi.l[w][r] * tc::ex2_approx(mi.m[w][r] - (top == -INFINITY ? 0.f : top));
       if (!whole) {
         reinterpret_cast<float4*>(a.part_o)[part * (kRows * D / 4) + e] = y;
@@ -575,10 +628,10 @@ __global__ void __launch_bounds__(kThreads, 2)
           a.part_ml[part * 2 * kRows + kRows + r] = all;
         }
       } else if (row0 + r < a.rows) {
-        const float inv = all == 0.f || (row0 + r) % a.T >= n ? 0.f : 1.f / all;
-        uint2 v = make_uint2(pack_bf16(y.x * inv, y.y * inv), pack_bf16(y.z * inv, y.w * inv));
-        if ((row0 + r) % a.T >= n) v = make_uint2(0u, 0u);
-        *reinterpret_cast<uint2*>(a.out + (qrow0 + row0 + r) * D + 4 * d4) = v;
+        const bool empty = all == 0.f || (row0 + r) % a.T >= n;
+        const float inv = 1.f / all;
+        *reinterpret_cast<uint2*>(a.out + (qrow0 + row0 + r) * D + 4 * d4) =
+            empty ? make_uint2(0u, 0u) : make_uint2(pack_bf16(y.x * inv, y.y * inv), pack_bf16(y.z * inv, y.w * inv));
         if (d4 == 0 && a.lse != nullptr) a.lse[qrow0 + row0 + r] = log2_sum(top, all);
       }
     }
@@ -599,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 // ---------------------------------------------------------------------------
 // One CTA a (segment, row): its warps take the partials in turn, a lane D / 32 columns.
 template <int D>
-__global__ void __launch_bounds__(kThreads) join_kernel(const CacheView c, const Step a, unsigned ctas) {
+__global__ void __launch_bounds__(kThreads) join_kernel(const CacheView c, const Step a, unsigned ctas, int kRows) {
   constexpr int E = D / 32;
   extern __shared__ char raw[];
   __shared__ int warp_sums[kWarps];
@@ -671,32 +724,25 @@ __global__ void __launch_bounds__(kThreads) weight_kernel(const CacheView c, con
     if (j < 0) continue;
     const int page = c.table[(size_t)b * c.max_blocks + j];
     if (page < 0 || page >= c.n_pages) continue;  // reported by the attention kernel
-    const size_t qrow0 = ((size_t)b * c.H + (size_t)hk * c.group) * a.T;
-    const float2* s = reinterpret_cast<const float2*>(a.scores + (size_t)t * a.rows * kBlock) + lane;
-    const float* lse = a.lse + qrow0;
+    const float* lse = a.lse + ((size_t)b * c.H + (size_t)hk * c.group) * a.T;
+    const float4* s = reinterpret_cast<const float4*>(a.scores + ((size_t)t * kBlock + lane) * a.score_rows);
+    const int half = 32 * a.score_rows / 4;  // from slot lane to slot lane + 32
     float x = 0.f, y = 0.f;
-    for (int g = 0; g < c.group; ++g)
-#pragma unroll 4
-      for (int i = 0; i < n; ++i) {
-        const int r = g * a.T + i;
-        const float2 v = s[r * (kBlock / 2)];
-        const float z = lse[r];
+    for (int r = 0; r < a.rows; r += 4) {
+      const float4 u = s[r / 4], v = s[r / 4 + half];
+      const float us[4] = {u.x, u.y, u.z, u.w}, vs[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float z = r + e < a.rows && (r + e) % a.T < n ? lse[r + e] : -INFINITY;
         if (z != -INFINITY) {
-          x += tc::ex2_approx(v.x - z);
-          y += tc::ex2_approx(v.y - z);
+          x += tc::ex2_approx(us[e] - z);
+          y += tc::ex2_approx(vs[e] - z);
         }
       }
-    const int slot = j * kBlock + 2 * lane;
-    float* w = c.weight + ((size_t)b * c.H_kv + hk) * c.cap + slot;
-    if (slot + 1 < L) {
-      float2* w2 = reinterpret_cast<float2*>(w);
-      float2 v = *w2;
-      v.x += x;
-      v.y += y;
-      *w2 = v;
-    } else if (slot < L) {
-      *w += x;
     }
+    float* w = c.weight + ((size_t)b * c.H_kv + hk) * c.cap + j * kBlock + lane;
+    if (j * kBlock + lane < L) *w += x;
+    if (j * kBlock + lane + 32 < L) w[32] += y;
   }
 }
 
@@ -714,7 +760,7 @@ constexpr int kMaxCtas = 2 * 148;  // a workspace is sized for this grid, whatev
 
 struct Layout {
   size_t ml, o, lse, scores, total;
-  int rows, groups;
+  int rows, group_rows, groups;
 };
 
 // Most tiles that a (sequence, KV head) can have.
@@ -731,7 +777,8 @@ sla_status plan_step(const sla_cache_config* c, int32_t T, int32_t top_n, int32_
   const int64_t rows = (int64_t)T * (c->H / c->H_kv);
   if (T > kCacheMaxT || rows > kCacheMaxRows || top_n > kCacheMaxSel) return SLA_ERR_UNSUPPORTED;
   p->rows = (int)rows;
-  p->groups = (p->rows + kRows - 1) / kRows;
+  p->group_rows = p->rows <= 8 ? 8 : 16;
+  p->groups = (p->rows + p->group_rows - 1) / p->group_rows;
   const int64_t segs = (int64_t)c->B * c->H_kv * p->groups;
   const int64_t tiles = (int64_t)c->B * c->H_kv * most_tiles(c, T, top_n, window);
   if (tiles * p->groups >= ((int64_t)1 << 31)) return SLA_ERR_UNSUPPORTED;  // the line is counted in 32 bits
@@ -742,10 +789,10 @@ sla_status plan_step(const sla_cache_config* c, int32_t T, int32_t top_n, int32_
     return o;
   };
   const size_t parts = kMaxCtas + (size_t)segs;
-  p->ml = take(parts * 2 * kRows * 4);
-  p->o = take(parts * kRows * c->d * 4);
+  p->ml = take(parts * 2 * p->group_rows * 4);
+  p->o = take(parts * p->group_rows * c->d * 4);
   p->lse = take(weights ? (size_t)c->B * c->H * T * 4 : 0);
-  p->scores = take(weights ? (size_t)tiles * p->rows * kBlock * 4 : 0);
+  p->scores = take(weights ? (size_t)tiles * align_up(p->rows, 8) * kBlock * 4 : 0);
   p->total = off;
   return SLA_OK;
 }
@@ -763,27 +810,32 @@ cudaError_t launch_after(cudaLaunchConfig_t* cfg, dim3 grid, size_t smem, cudaSt
   return cudaSuccess;
 }
 
-template <int KIND, int D>
+template <int KIND, int D, int NR>
 cudaError_t launch(const CacheView& c, const Step& a, int sms, cudaStream_t s) {
   CUtensorMap kmap, vmap;
   const uint64_t rows = (uint64_t)c.n_pages * c.H_kv * kBlock;
   if (!make_tmap_rows_u8(&kmap, c.k, rows, D, kBlock) || !make_tmap_rows_u8(&vmap, c.v, rows, D, kBlock))
     return cudaErrorInvalidValue;
-  auto attend = attend_kernel<KIND, D>;
-  cudaError_t e = cudaFuncSetAttribute(attend, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Smem<D>::bytes(kCacheMaxB));
+  auto attend = attend_kernel<KIND, D, NR>;
+  cudaError_t e = cudaFuncSetAttribute(attend, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Smem<D, NR>::bytes(kCacheMaxB));
   if (e != cudaSuccess) return e;
   const int ctas = 2 * sms < kMaxCtas ? 2 * sms : kMaxCtas;
-  attend<<<ctas, kThreads, Smem<D>::bytes(c.B), s>>>(kmap, vmap, c, a);
+  attend<<<ctas, kThreads, Smem<D, NR>::bytes(c.B), s>>>(kmap, vmap, c, a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute at[1];
   const int segs = c.B * c.H_kv * a.groups;
-  launch_after(&cfg, dim3(segs, a.rows < kRows ? a.rows : kRows), lines_bytes(c.B), s, at);
-  e = cudaLaunchKernelEx(&cfg, join_kernel<D>, c, a, (unsigned)ctas);
+  launch_after(&cfg, dim3(segs, a.rows < 8 * NR ? a.rows : 8 * NR), lines_bytes(c.B), s, at);
+  e = cudaLaunchKernelEx(&cfg, join_kernel<D>, c, a, (unsigned)ctas, 8 * NR);
   if (e != cudaSuccess || c.weight == nullptr) return e;
   launch_after(&cfg, dim3(8 * sms), lines_bytes(c.B), s, at);
   return cudaLaunchKernelEx(&cfg, weight_kernel, c, a);
+}
+
+template <int KIND, int D>
+cudaError_t launch_rows(const CacheView& c, const Step& a, int group_rows, int sms, cudaStream_t s) {
+  return group_rows == 8 ? launch<KIND, D, 1>(c, a, sms, s) : launch<KIND, D, 2>(c, a, sms, s);
 }
 
 }  // namespace
@@ -828,14 +880,17 @@ sla_status sla_cache_attend(const void* q, const sla_cache_config* cfg, const sl
   a.window = window < c.cap + kCacheMaxT ? window : c.cap + kCacheMaxT;  // more sees no more
   a.rows = p.rows;
   a.groups = p.groups;
+  a.score_rows = (int)align_up(p.rows, 8);
   const int sms = sm_count();
   if (sms < 1) return SLA_ERR_CUDA;
   cudaStream_t s = (cudaStream_t)stream;
   cudaError_t e;
   if (c.kind == SLA_CACHE_E4M3)
-    e = c.d == 128 ? launch<SLA_CACHE_E4M3, 128>(c, a, sms, s) : launch<SLA_CACHE_E4M3, 64>(c, a, sms, s);
+    e = c.d == 128 ? launch_rows<SLA_CACHE_E4M3, 128>(c, a, p.group_rows, sms, s)
+                   : launch_rows<SLA_CACHE_E4M3, 64>(c, a, p.group_rows, sms, s);
   else
-    e = c.d == 128 ? launch<SLA_CACHE_INT8, 128>(c, a, sms, s) : launch<SLA_CACHE_INT8, 64>(c, a, sms, s);
+    e = c.d == 128 ? launch_rows<SLA_CACHE_INT8, 128>(c, a, p.group_rows, sms, s)
+                   : launch_rows<SLA_CACHE_INT8, 64>(c, a, p.group_rows, sms, s);
   return e == cudaSuccess ? SLA_OK : SLA_ERR_CUDA;
 }
 
