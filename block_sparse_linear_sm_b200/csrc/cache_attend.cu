@@ -34,8 +34,8 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kSlots = 2;       // pages in a warp's ring
-constexpr int kInfo = 4;        // described tiles ahead (at most kSlots + 1 are in use)
+constexpr int kSlots = 2;       // pages in a warp's ring: keys and values of a tile
+constexpr int kCtasPerSm = 2;
 constexpr int kMinRun = kWarps;  // tiles a CTA takes at least
 constexpr float kShift = 15.f;
 
@@ -209,22 +209,40 @@ __device__ __forceinline__ float log2_sum(float m, float l) { return l == 0.f ? 
 // ---------------------------------------------------------------------------
 // a warp's ring
 // ---------------------------------------------------------------------------
-struct TileInfo {
-  int seg, block, ph;  // segment of the line, block of the sequence, page * H_kv + hk
-  int tile;            // number of the tile among those of all (sequence, KV head)
-  int chosen;
+// All of it is the same in every lane.
+struct Tile {
+  int seg, block;  // segment of the line, block of the sequence
+  int tile;        // number of the tile among those of all (sequence, KV head)
+  bool chosen;     // the window does not limit it
 };
 
 template <int D>
 struct Ring {
   static constexpr int kPage = kBlock * D;  // bytes of a page of one head
   uint32_t data, bars;                      // shared addresses: kSlots pages, kSlots barriers
-  TileInfo* info;                           // [kInfo]
   unsigned issued, used;                    // pages requested and released (K and V of a tile in turn)
-  unsigned next, end;                       // tiles of the line still to be described
-  int seq;                                  // sequence of tile `next`
-  int vrow;                                 // page whose values are requested next, -1: describe a tile
+  unsigned next, end;                       // tiles of the line not yet looked at
+  // where tile `next` is: its sequence, KV head, segment, number in it, the segment's tiles
+  int b, hk, seg, idx, nb;
+  int vrow;  // first row of the values requested next
+  // the tile whose pages are requested, and the one after it, whose table entry is being loaded
+  Tile req, ahead;
+  int ahead_page, ahead_hk;
+  float req_ks, req_vs;
+  bool has_req, has_ahead;
 };
+
+// Places the ring's `next` in its segment.
+template <int D>
+__device__ __forceinline__ void locate(Ring<D>& r, const CacheView& c, const Step& a, const Lines& l) {
+  const unsigned per = c.H_kv * a.groups;
+  while ((unsigned)l.cum[r.b + 1] * per <= r.next) ++r.b;
+  r.nb = l.cum[r.b + 1] - l.cum[r.b];
+  const unsigned in = r.next - (unsigned)l.cum[r.b] * per, sr = in / (unsigned)r.nb;
+  r.hk = a.groups == 1 ? (int)sr : (int)sr / a.groups;
+  r.idx = (int)(in - sr * r.nb);
+  r.seg = r.b * (int)per + (int)sr;
+}
 
 template <int D>
 __device__ __forceinline__ void request(Ring<D>& r, const CUtensorMap* map, int row, int lane) {
@@ -236,47 +254,49 @@ __device__ __forceinline__ void request(Ring<D>& r, const CUtensorMap* map, int 
   ++r.issued;
 }
 
-// Requests pages until the ring is full or the run ends. Called by the whole warp, after
-// every lane has finished with the released pages.
+// Finds the run's next tile that names a block and starts to load its table entry.
 template <int D>
-__device__ __forceinline__ void pump(Ring<D>& r, const CacheView& c, const Step& a, const Lines& l,
-                                     const CUtensorMap* kmap, const CUtensorMap* vmap, int lane) {
-  __syncwarp();
-  while (r.issued - r.used < kSlots) {
-    if (r.vrow >= 0) {
-      request(r, vmap, r.vrow, lane);
-      r.vrow = -1;
-      continue;
-    }
-    if (r.next >= r.end) break;
-    const unsigned per = c.H_kv * a.groups;
-    while ((unsigned)l.cum[r.seq + 1] * per <= r.next) ++r.seq;
-    const int b = r.seq, nb = l.cum[b + 1] - l.cum[b];
-    const unsigned in = r.next - (unsigned)l.cum[b] * per, sr = in / (unsigned)nb;
-    const int hk = (int)sr / a.groups;
+__device__ __forceinline__ void look_ahead(Ring<D>& r, const CacheView& c, const Step& a, const Lines& l, int lane) {
+  r.has_ahead = false;
+  while (r.next < r.end && !r.has_ahead) {
+    if (r.idx >= r.nb) locate(r, c, a, l);
     bool chosen;
-    const int idx = (int)(in - sr * nb);
-    const int j = tile_block(c, a, b, hk, idx, l.len[b], l.fresh[b], lane, &chosen);
+    const int j = tile_block(c, a, r.b, r.hk, r.idx, l.len[r.b], l.fresh[r.b], lane, &chosen);
+    if (j >= 0) {
+      r.ahead.seg = r.seg;
+      r.ahead.block = j;
+      r.ahead.tile = l.cum[r.b] * c.H_kv + r.hk * r.nb + r.idx;
+      r.ahead.chosen = chosen;
+      r.ahead_hk = r.hk;
+      r.ahead_page = c.table[(size_t)r.b * c.max_blocks + j];
+      r.has_ahead = true;
+    }
     r.next += kWarps;
-    if (j < 0) continue;
-    const int page = c.table[(size_t)b * c.max_blocks + j];
-    if (page < 0 || page >= c.n_pages) {
-      if (lane == 0) report(c.status, SLA_ERR_DEVICE_CHECK, kDetailCachePage);
-      continue;
-    }
-    const int ph = page * c.H_kv + hk;
-    if (lane == 0) {
-      TileInfo* t = &r.info[(r.issued / 2) % kInfo];
-      t->seg = b * (int)per + (int)sr;
-      t->block = j;
-      t->ph = ph;
-      t->tile = l.cum[b] * c.H_kv + hk * nb + idx;
-      t->chosen = chosen;
-    }
-    request(r, kmap, ph * kBlock, lane);
-    r.vrow = ph * kBlock;
+    r.idx += kWarps;
   }
-  __syncwarp();
+}
+
+// Requests the keys of the tile ahead, if there is one, and looks for the one after it.
+template <int D>
+__device__ __forceinline__ void request_keys(Ring<D>& r, const CacheView& c, const Step& a, const Lines& l,
+                                             const CUtensorMap* kmap, int lane) {
+  r.has_req = false;
+  while (r.has_ahead) {
+    const int page = r.ahead_page;
+    if (page >= 0 && page < c.n_pages) {
+      const int ph = page * c.H_kv + r.ahead_hk;
+      request(r, kmap, ph * kBlock, lane);
+      r.vrow = ph * kBlock;
+      r.req = r.ahead;
+      r.req_ks = c.k_scale[ph];
+      r.req_vs = c.v_scale[ph];
+      r.has_req = true;
+      look_ahead(r, c, a, l, lane);
+      return;
+    }
+    if (lane == 0) report(c.status, SLA_ERR_DEVICE_CHECK, kDetailCachePage);
+    look_ahead(r, c, a, l, lane);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -286,28 +306,44 @@ template <int D, int NR>
 struct Smem {
   static constexpr int kPitch = D + 4;  // words of a merged row: lanes of a store hit all banks
   static constexpr int kRing = kWarps * kSlots * kBlock * D;
-  static constexpr int kMerge = kWarps * 8 * NR * kPitch * 4;
-  static constexpr int off_merge = kRing, off_misc = kRing + kMerge;
-  static constexpr int kMisc = 2048;
+  static constexpr int kMerge = kWarps * 8 * NR * kPitch * 4;  // the warps' outputs
+  static constexpr int kQ = 8 * NR * D * 2;                    // Q's fragments; the next segment's rows
+  static constexpr int off_merge = kRing, off_q = off_merge + kMerge, off_next_q = off_q + kQ, off_misc = off_next_q + kQ;
+  static constexpr int kMisc = 1280;
   static constexpr int off_lines = off_misc + kMisc;
-  static size_t bytes(int B) { return off_lines + lines_bytes(B) + 1024; }
+  static size_t bytes(int B) { return off_lines + lines_bytes(B); }
 };
+
+// A segment of the line: one row group of one KV head of one sequence, with its tiles.
+struct Segment {
+  int b, sr;         // sequence, number in it
+  unsigned lo, nb;   // first tile of the line, tiles
+};
+__device__ __forceinline__ void next_segment(Segment& s, const Lines& l, unsigned per) {
+  s.lo += s.nb;
+  if (++s.sr == (int)per) {
+    s.sr = 0;
+    do ++s.b;
+    while (l.cum[s.b + 1] == l.cum[s.b]);  // there is a tile ahead, so there is such a sequence
+    s.nb = l.cum[s.b + 1] - l.cum[s.b];
+  }
+}
 
 // NR: query rows of a segment in eights.
 template <int KIND, int D, int NR>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
     attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const CacheView c,
                   const Step a) {
   constexpr int KS = D / 16;  // k steps of K Q^T; words of codes a lane holds of a key row
   constexpr int MT = D / 16;  // row tiles of O^T
   constexpr int kRows = 8 * NR;
   using Sm = Smem<D, NR>;
-  extern __shared__ char raw[];
-  char* smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+  extern __shared__ __align__(1024) char smem[];  // TMA's swizzle goes by address bits
   struct Misc {
     uint64_t bars[kWarps][kSlots];
-    TileInfo info[kWarps][kInfo];
     float m[kWarps][kRows], l[kWarps][kRows];
+    float qs[kRows];  // what a row's scores are multiplied by
+    float top[kRows], all[kRows];  // the segment's
     int warp_sums[kWarps];
     int abort, never;
   };
@@ -336,70 +372,87 @@ __global__ void __launch_bounds__(kThreads, 2)
   Ring<D> ring;
   ring.data = smem_u32(smem) + warp * kSlots * Ring<D>::kPage;
   ring.bars = smem_u32(&mi.bars[warp][0]);
-  ring.info = mi.info[warp];
   ring.issued = ring.used = 0;
   ring.next = lo + warp;
   ring.end = hi;
-  ring.seq = find_sequence(l, c.B, lo, per);
-  ring.vrow = -1;
-  int b = ring.seq;
-  pump(ring, c, a, l, &kmap, &vmap, lane);
+  Segment sg;
+  sg.b = find_sequence(l, c.B, lo, per);
+  sg.nb = l.cum[sg.b + 1] - l.cum[sg.b];
+  sg.sr = (int)((lo - (unsigned)l.cum[sg.b] * per) / sg.nb);
+  sg.lo = (unsigned)l.cum[sg.b] * per + sg.sr * sg.nb;
+  // rows of Q, eight by a warp: lane (g, q4) copies row g's elements q4 * D / 4 .. for itself
+  const uint32_t my_q = smem_u32(smem + Sm::off_next_q) + (warp * 32 + lane) * (D / 2);
+  auto fetch_q = [&](const Segment& s) {
+    const int hk = a.groups == 1 ? s.sr : s.sr / a.groups, grp = s.sr - hk * a.groups;
+    const int r = grp * kRows + 8 * warp + g;
+    if (warp < NR && r < a.rows) {
+      const __nv_bfloat16* p = a.q + (((size_t)s.b * c.H + (size_t)hk * c.group) * a.T + r) * D + q4 * (D / 4);
+#pragma unroll
+      for (int u = 0; u < D / 32; ++u) cp_async16(my_q + 16 * u, p + 8 * u, 16);
+    }
+    cp_async_commit();
+  };
+  fetch_q(sg);
+  ring.b = sg.b;
+  ring.idx = ring.nb = 0;  // locate it first
+  // the first tile's keys and values
+  look_ahead(ring, c, a, l, lane);
+  request_keys(ring, c, a, l, &kmap, lane);
+  if (ring.has_req) request(ring, &vmap, ring.vrow, lane);
 
   float* merge = reinterpret_cast<float*>(smem + Sm::off_merge);
   bool dead = false;
-  unsigned at = lo;  // first tile of the segment being worked on
-  while (at < hi) {
-    while ((unsigned)l.cum[b + 1] * per <= at) ++b;
-    const int nb = l.cum[b + 1] - l.cum[b], L = l.len[b], n = l.fresh[b];
-    const unsigned sr = (at - (unsigned)l.cum[b] * per) / (unsigned)nb;
-    const int hk = (int)sr / a.groups, grp = (int)sr % a.groups, seg = b * (int)per + (int)sr;
-    const unsigned seg_lo = (unsigned)l.cum[b] * per + sr * nb, seg_hi = seg_lo + nb;
-    const int row0 = grp * kRows;
-    const size_t qrow0 = ((size_t)b * c.H + (size_t)hk * c.group) * a.T;
+  while (sg.lo < hi) {
+    const int L = l.len[sg.b], n = l.fresh[sg.b], seg = sg.b * (int)per + sg.sr;
+    const int hk = a.groups == 1 ? sg.sr : sg.sr / a.groups, row0 = (sg.sr - hk * a.groups) * kRows;
+    const unsigned seg_lo = sg.lo, seg_hi = sg.lo + sg.nb;
+    const size_t qrow0 = ((size_t)sg.b * c.H + (size_t)hk * c.group) * a.T;
 
-    // Q^T's columns: this lane holds row g of each eight, d = q4 * D / 4 ..
-    uint32_t qf[NR][KS][2];
-    float qs[NR][2];  // scale of the rows whose scores this lane gets: 8 i + 2 q4 + e
-    int pos[NR][2];   // the slots such a row sees end here
+    // Q^T's columns go where the product's lanes find them
+    uint2* qf = reinterpret_cast<uint2*>(smem + Sm::off_q);  // [NR][KS][32]
+    cp_async_wait<0>();
+    if (warp < NR) {
+      const bool there = row0 + 8 * warp + g < a.rows;
+      float x[D / 4], top = 0.f;
 #pragma unroll
-    for (int i = 0; i < NR; ++i) {
-      const int r = row0 + 8 * i + g;
-      float x[D / 4];
+      for (int u = 0; u < D / 32; ++u) {
+        const uint4 w = lds128(my_q + 16 * u);
+        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-      for (int e = 0; e < D / 4; ++e) x[e] = 0.f;
-      if (r < a.rows) {
-        const uint4* p = reinterpret_cast<const uint4*>(a.q + (qrow0 + r) * D + q4 * (D / 4));
-#pragma unroll
-        for (int u = 0; u < D / 32; ++u) {
-          const uint4 w = p[u];
-          const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 f = unpack_bf16(ws[e]);
-            x[8 * u + 2 * e] = f.x;
-            x[8 * u + 2 * e + 1] = f.y;
-          }
+        for (int e = 0; e < 4; ++e) {
+          const float2 f = unpack_bf16(there ? ws[e] : 0u);
+          x[8 * u + 2 * e] = f.x;
+          x[8 * u + 2 * e + 1] = f.y;
+          top = tc::fmax3(top, fabsf(f.x), fabsf(f.y));
         }
       }
-      float top = 0.f;
-#pragma unroll
-      for (int e = 0; e < D / 4; ++e) top = fmaxf(top, fabsf(x[e]));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
       const int ex = max((int)(__float_as_uint(top) >> 23) - 127, -100);
-      const float up = exp2_int(14 - ex), down = exp2_int(ex - 14) * (c.scale * 1.4426950408889634f);
+      const float up = exp2_int(14 - ex);
+      if (q4 == 0) mi.qs[8 * warp + g] = exp2_int(ex - 14) * (c.scale * 1.4426950408889634f);
 #pragma unroll
-      for (int s = 0; s < KS; ++s) {
-        qf[i][s][0] = pack_f16(x[4 * s] * up, x[4 * s + 1] * up);
-        qf[i][s][1] = pack_f16(x[4 * s + 2] * up, x[4 * s + 3] * up);
-      }
+      for (int s = 0; s < KS; ++s)
+        qf[(warp * KS + s) * 32 + lane] =
+            make_uint2(pack_f16(x[4 * s] * up, x[4 * s + 1] * up), pack_f16(x[4 * s + 2] * up, x[4 * s + 3] * up));
+    }
+    __syncthreads();
+    if (seg_hi < hi) {
+      next_segment(sg, l, per);
+      fetch_q(sg);
+    } else {
+      sg.lo = hi;
+    }
+    float qs[NR][2];  // of the rows whose scores this lane gets: 8 i + 2 q4 + e
+    int pos[NR][2];   // the slots such a row sees end here
+#pragma unroll
+    for (int i = 0; i < NR; ++i)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int col = 2 * q4 + e, rc = row0 + 8 * i + col, t = rc % a.T;
-        qs[i][e] = __shfl_sync(0xffffffffu, down, 4 * col);
+        const int col = 8 * i + 2 * q4 + e, rc = row0 + col, t = a.T == 1 ? 0 : rc % a.T;
+        qs[i][e] = mi.qs[col];
         pos[i][e] = rc < a.rows && t < n ? L - n + t : -1;
       }
-    }
 
     float o[MT][NR][4], m[NR][2], sum[NR][2];
 #pragma unroll
@@ -410,12 +463,11 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int t = 0; t < MT; ++t) o[t][i][0] = o[t][i][1] = o[t][i][2] = o[t][i][3] = 0.f;
     }
 
-    while (ring.used < ring.issued) {
-      const TileInfo* ti = &ring.info[(ring.used / 2) % kInfo];
-      if (ti->seg != seg) break;
-      const int j0 = ti->block * kBlock, ph = ti->ph, tile = ti->tile;
-      const bool chosen = ti->chosen;
-      const float ks = c.k_scale[ph], vs = c.v_scale[ph] * exp2_int(-(int)kShift);
+    while (ring.has_req && ring.req.seg == seg) {
+      const Tile cur = ring.req;
+      const int j0 = cur.block * kBlock;
+      const bool chosen = cur.chosen;
+      const float ks = ring.req_ks, vs = ring.req_vs * exp2_int(-(int)kShift);
       const uint32_t slot_k = ring.used % kSlots;
       if (!dead && !tc::mbar_wait(ring.bars + 8 * slot_k, (ring.used / kSlots) & 1, &mi.abort)) dead = true;
       const uint32_t kbase = ring.data + slot_k * Ring<D>::kPage;
@@ -427,7 +479,12 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
         for (int i = 0; i < NR; ++i) s[t][i][0] = s[t][i][1] = s[t][i][2] = s[t][i][3] = 0.f;
 #pragma unroll
-      for (int u = 0; u < D / 64; ++u)
+      for (int u = 0; u < D / 64; ++u) {
+        uint2 qk[NR][4];
+#pragma unroll
+        for (int i = 0; i < NR; ++i)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) qk[i][k] = qf[(i * KS + 4 * u + k) * 32 + lane];
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
           const int row = 16 * t + 4 * (g >> 1) + (g & 1);
@@ -446,11 +503,13 @@ __global__ void __launch_bounds__(kThreads, 2)
             decode4_f16<KIND>(xs[k], f[0], f[2]);
             decode4_f16<KIND>(ys[k], f[1], f[3]);
 #pragma unroll
-            for (int i = 0; i < NR; ++i) mma_f16(s[t][i], f, qf[i][4 * u + k][0], qf[i][4 * u + k][1]);
+            for (int i = 0; i < NR; ++i) mma_f16(s[t][i], f, qk[i][k].x, qk[i][k].y);
           }
         }
+      }
       ++ring.used;
-      pump(ring, c, a, l, &kmap, &vmap, lane);
+      __syncwarp();  // every lane has finished with the keys
+      request_keys(ring, c, a, l, &kmap, lane);
 
       // rows that do not see the whole page: its end, the window's start
       if (j0 + kBlock - 1 > L - n || (!chosen && j0 <= L - 1 - a.window)) {
@@ -494,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const int slot = 16 * t + 4 * (g >> 1) + (g & 1) + 2 * h;
-              *reinterpret_cast<float2*>(a.scores + ((size_t)tile * kBlock + slot) * a.score_rows + row0 + 8 * i + 2 * q4) =
+              *reinterpret_cast<float2*>(a.scores + ((size_t)cur.tile * kBlock + slot) * a.score_rows + row0 + 8 * i + 2 * q4) =
                   make_float2(s[t][i][2 * h] * f[0], s[t][i][2 * h + 1] * f[1]);
             }
         }
@@ -569,7 +628,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       ++ring.used;
       if (j0 + kBlock > L) tc::fence_async_smem();  // the zeros come before the page that is loaded next
-      pump(ring, c, a, l, &kmap, &vmap, lane);
+      __syncwarp();
+      if (ring.has_req) request(ring, &vmap, ring.vrow, lane);
     }
 
     // the warps' parts of the segment become one
@@ -602,25 +662,29 @@ __global__ void __launch_bounds__(kThreads, 2)
           p[16 * t] = o[t][i][e] * f;
           p[16 * t + 8] = o[t][i][e + 2] * f;
         }
+        if (warp == kWarps - 1 && g == 0) {
+          float all = 0.f;
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) all += mi.l[w][r] * tc::ex2_approx(mi.m[w][r] - (top == -INFINITY ? 0.f : top));
+          mi.top[r] = top;
+          mi.all[r] = all;
+        }
       }
     __syncthreads();
     const bool whole = seg_lo >= lo && seg_hi <= hi;
     const size_t part = (size_t)blockIdx.x + seg;
     for (int e = tid; e < kRows * D / 4; e += kThreads) {
       const int r = e / (D / 4), d4 = e % (D / 4);
-      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-      float top = mi.m[0][r], all = 0.f;
+      float4 y = *reinterpret_cast<const float4*>(merge + r * Sm::kPitch + 4 * d4);
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
+      for (int w = 1; w < kWarps; ++w) {
         const float4 x = *reinterpret_cast<const float4*>(merge + (w * kRows + r) * Sm::kPitch + 4 * d4);
         y.x += x.x;
         y.y += x.y;
         y.z += x.z;
         y.w += x.w;
-        top = fmaxf(top, mi.m[w][r]);
       }
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) all += mi.l[w][r] * tc::ex2_approx(mi.m[w][r] - (top == -INFINITY ? 0.f : top));
+      const float top = mi.top[r], all = mi.all[r];
       if (!whole) {
         reinterpret_cast<float4*>(a.part_o)[part * (kRows * D / 4) + e] = y;
         if (d4 == 0) {
@@ -635,8 +699,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (d4 == 0 && a.lse != nullptr) a.lse[qrow0 + row0 + r] = log2_sum(top, all);
       }
     }
-    at = seg_hi;
-    __syncthreads();  // merge, m and l are free again
+    // what is written here is written again behind the next segment's first barrier
   }
   if (dead) {
     mi.abort = 1;
@@ -650,57 +713,69 @@ __global__ void __launch_bounds__(kThreads, 2)
 // ---------------------------------------------------------------------------
 // segments that several CTAs worked on, or none
 // ---------------------------------------------------------------------------
-// One CTA a (segment, row): its warps take the partials in turn, a lane D / 32 columns.
-template <int D>
-__global__ void __launch_bounds__(kThreads) join_kernel(const CacheView c, const Step a, unsigned ctas, int kRows) {
-  constexpr int E = D / 32;
-  extern __shared__ char raw[];
-  __shared__ int warp_sums[kWarps];
-  __shared__ float s_l[kWarps], s_o[kWarps][D];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+// PW warps a row take the partials in turn, a lane D / 32 columns; a CTA has 8 / PW rows.
+constexpr int kJoinThreads = 256;
+
+template <int D, int PW>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const CacheView c, const Step a, unsigned ctas, int rows) {
+  constexpr int E = D / 32, W = kJoinThreads / 32;
+  extern __shared__ __align__(1024) char smem[];
+  __shared__ int warp_sums[W];
+  __shared__ float s_l[W], s_o[PW > 1 ? W : 1][D];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, part_warp = warp % PW;
   Lines l;
-  scan_lines(c, a, raw, &l, warp_sums);
+  scan_lines(c, a, smem, &l, warp_sums);
   const unsigned per = c.H_kv * a.groups, total = (unsigned)l.cum[c.B] * per;
   const unsigned run = max((total + ctas - 1) / ctas, (unsigned)kMinRun);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;");
-  const int seg = blockIdx.x, b = seg / (int)per, sr = seg % (int)per, hk = sr / a.groups, r = blockIdx.y;
-  const int row = sr % a.groups * kRows + r;
-  if (row >= a.rows) return;
-  const size_t qrow = ((size_t)b * c.H + (size_t)hk * c.group) * a.T + row;
+  const int seg = blockIdx.x, b = seg / (int)per, sr = seg % (int)per, hk = sr / a.groups;
+  const int r = blockIdx.y * (W / PW) + warp / PW, row = sr % a.groups * rows + r;
   const int nb = l.cum[b + 1] - l.cum[b];
   const unsigned lo = (unsigned)l.cum[b] * per + (unsigned)sr * nb, hi = lo + nb;
   const unsigned c0 = nb ? lo / run : 0, c1 = nb ? (hi - 1) / run : 0;
+  const size_t qrow = ((size_t)b * c.H + (size_t)hk * c.group) * a.T + row;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
   if (nb != 0 && c0 == c1) return;  // written by the CTA that had all of it
+  const bool there = r < rows && row < a.rows;
   float m = -INFINITY, sum = 0.f, o[E];
+#pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.f;
-  if (nb != 0) {
-    for (unsigned i = c0 + lane; i <= c1; i += 32) m = fmaxf(m, a.part_ml[((size_t)i + seg) * 2 * kRows + r]);
+  if (nb != 0 && there) {
+    for (unsigned i = c0 + lane; i <= c1; i += 32) m = fmaxf(m, a.part_ml[((size_t)i + seg) * 2 * rows + r]);
     for (int s = 16; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
     const float top = m == -INFINITY ? 0.f : m;
 #pragma unroll 4
-    for (unsigned i = c0 + warp; i <= c1; i += kWarps) {
+    for (unsigned i = c0 + part_warp; i <= c1; i += PW) {
       const size_t part = (size_t)i + seg;
-      const float f = tc::ex2_approx(a.part_ml[part * 2 * kRows + r] - top);
-      sum += a.part_ml[part * 2 * kRows + kRows + r] * f;
-      const float* p = a.part_o + (part * kRows + r) * D + lane * E;
+      const float f = tc::ex2_approx(a.part_ml[part * 2 * rows + r] - top);
+      sum += a.part_ml[part * 2 * rows + rows + r] * f;
+      const float* p = a.part_o + (part * rows + r) * D + lane * E;
 #pragma unroll
       for (int e = 0; e < E; ++e) o[e] += p[e] * f;
     }
   }
-  if (lane == 0) s_l[warp] = sum;
+  if (PW > 1) {
+    if (lane == 0) s_l[warp] = sum;
 #pragma unroll
-  for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = o[e];
-  __syncthreads();
-  sum = 0.f;
-  for (int w = 0; w < kWarps; ++w) sum += s_l[w];
-  const bool valid = row % a.T < l.fresh[b] && sum != 0.f;
-  if (tid < D) {
-    float y = 0.f;
-    for (int w = 0; w < kWarps; ++w) y += s_o[w][tid];
-    a.out[qrow * D + tid] = __float2bfloat16(valid ? y / sum : 0.f);
+    for (int e = 0; e < E; ++e) s_o[PW > 1 ? warp : 0][lane * E + e] = o[e];
+    __syncthreads();
+    if (part_warp != 0) return;
+    sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < PW; ++w) sum += s_l[warp + w];
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      o[e] = 0.f;
+#pragma unroll
+      for (int w = 0; w < PW; ++w) o[e] += s_o[PW > 1 ? warp + w : 0][lane * E + e];
+    }
   }
-  if (tid == 0 && a.lse != nullptr) a.lse[qrow] = log2_sum(m, sum);
+  if (!there) return;
+  const bool valid = row % a.T < l.fresh[b] && sum != 0.f;
+#pragma unroll
+  for (int e = 0; e < E; e += 2)
+    *reinterpret_cast<uint32_t*>(a.out + qrow * D + lane * E + e) = valid ? pack_bf16(o[e] / sum, o[e + 1] / sum) : 0u;
+  if (lane == 0 && a.lse != nullptr) a.lse[qrow] = log2_sum(m, sum);
 }
 
 // ---------------------------------------------------------------------------
@@ -708,11 +783,11 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const CacheView c, const
 // ---------------------------------------------------------------------------
 // A warp a tile (list entries that name no block are passed over), a lane two slots.
 __global__ void __launch_bounds__(kThreads) weight_kernel(const CacheView c, const Step a) {
-  extern __shared__ char raw[];
+  extern __shared__ __align__(1024) char smem[];
   __shared__ int warp_sums[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   Lines l;
-  scan_lines(c, a, raw, &l, warp_sums);
+  scan_lines(c, a, smem, &l, warp_sums);
   const unsigned per = c.H_kv, total = (unsigned)l.cum[c.B] * per;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   for (unsigned t = blockIdx.x * kWarps + warp; t < total; t += gridDim.x * kWarps) {
@@ -756,7 +831,7 @@ int sm_count() {
   return n;
 }
 
-constexpr int kMaxCtas = 2 * 148;  // a workspace is sized for this grid, whatever device is current
+constexpr int kMaxCtas = kCtasPerSm * 148;  // a workspace is sized for this grid, whatever device is current
 
 struct Layout {
   size_t ml, o, lse, scores, total;
@@ -797,17 +872,16 @@ sla_status plan_step(const sla_cache_config* c, int32_t T, int32_t top_n, int32_
   return SLA_OK;
 }
 
-cudaError_t launch_after(cudaLaunchConfig_t* cfg, dim3 grid, size_t smem, cudaStream_t s, cudaLaunchAttribute* at) {
+void launch_after(cudaLaunchConfig_t* cfg, dim3 grid, int threads, size_t smem, cudaStream_t s, cudaLaunchAttribute* at) {
   *cfg = cudaLaunchConfig_t{};
   cfg->gridDim = grid;
-  cfg->blockDim = dim3(kThreads);
+  cfg->blockDim = dim3(threads);
   cfg->dynamicSmemBytes = smem;
   cfg->stream = s;
   at->id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at->val.programmaticStreamSerializationAllowed = 1;
   cfg->attrs = at;
   cfg->numAttrs = 1;
-  return cudaSuccess;
 }
 
 template <int KIND, int D, int NR>
@@ -819,17 +893,24 @@ cudaError_t launch(const CacheView& c, const Step& a, int sms, cudaStream_t s) {
   auto attend = attend_kernel<KIND, D, NR>;
   cudaError_t e = cudaFuncSetAttribute(attend, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Smem<D, NR>::bytes(kCacheMaxB));
   if (e != cudaSuccess) return e;
-  const int ctas = 2 * sms < kMaxCtas ? 2 * sms : kMaxCtas;
+  const int ctas = kCtasPerSm * sms < kMaxCtas ? kCtasPerSm * sms : kMaxCtas;
   attend<<<ctas, kThreads, Smem<D, NR>::bytes(c.B), s>>>(kmap, vmap, c, a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute at[1];
   const int segs = c.B * c.H_kv * a.groups;
-  launch_after(&cfg, dim3(segs, a.rows < 8 * NR ? a.rows : 8 * NR), lines_bytes(c.B), s, at);
-  e = cudaLaunchKernelEx(&cfg, join_kernel<D>, c, a, (unsigned)ctas, 8 * NR);
+  const int most = a.rows < 8 * NR ? a.rows : 8 * NR;
+  // A warp a row where segments are cut into few parts, eight where one is spread over the device
+  if (ctas > 16 * segs) {
+    launch_after(&cfg, dim3(segs, most), kJoinThreads, lines_bytes(c.B), s, at);
+    e = cudaLaunchKernelEx(&cfg, join_kernel<D, 8>, c, a, (unsigned)ctas, 8 * NR);
+  } else {
+    launch_after(&cfg, dim3(segs, (most + 7) / 8), kJoinThreads, lines_bytes(c.B), s, at);
+    e = cudaLaunchKernelEx(&cfg, join_kernel<D, 1>, c, a, (unsigned)ctas, 8 * NR);
+  }
   if (e != cudaSuccess || c.weight == nullptr) return e;
-  launch_after(&cfg, dim3(8 * sms), lines_bytes(c.B), s, at);
+  launch_after(&cfg, dim3(8 * sms), kThreads, lines_bytes(c.B), s, at);
   return cudaLaunchKernelEx(&cfg, weight_kernel, c, a);
 }
 
