@@ -91,18 +91,44 @@ __device__ __forceinline__ uint4 recode16(const uint4& c, float ratio) {
   return encode16<KIND>(y, ratio);
 }
 
-// Mean of a page's 64 rows of codes in shared memory, times the scale. Codes are integers
-// times 2^-9 (e4m3) or integers (int8) of at most 19 bits, so 64 of them add up exactly in
-// fp32, in any order. All threads; parts: kCta * 4 floats.
+// Mean of a page's 64 rows of codes in shared memory, times the scale; all threads. Codes are
+// integers times 2^-9 (e4m3) or integers (int8) of at most 19 bits, so 64 of them add up
+// exactly, in any order: in fp32, or (int8, offset by 128) four at a time in 16-bit lanes.
 template <int KIND, int D>
 __device__ __forceinline__ void write_mean(const uint8_t* tile, float scale, float* mean, float4* parts) {
   constexpr int W = D / 4, P = kCta / W, R = kBlock / P;  // words a row, threads a word, rows a thread
   const int w = threadIdx.x % W, p = threadIdx.x / W;
+  const uint32_t* word = reinterpret_cast<const uint32_t*>(tile + p * R * D) + w;
+  const float f = scale * (1.f / kBlock);
+  if (KIND == SLA_CACHE_INT8) {
+    uint2* sums = reinterpret_cast<uint2*>(parts);
+    uint32_t even = 0, odd = 0;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const uint32_t u = word[r * W] ^ 0x80808080u;
+      even += u & 0x00ff00ffu;
+      odd += (u >> 8) & 0x00ff00ffu;
+    }
+    sums[threadIdx.x] = make_uint2(even, odd);
+    __syncthreads();
+    if (threadIdx.x < W) {
+#pragma unroll
+      for (int i = 1; i < P; ++i) {
+        even += sums[i * W + threadIdx.x].x;
+        odd += sums[i * W + threadIdx.x].y;
+      }
+      constexpr int kOff = 128 * kBlock;
+      reinterpret_cast<float4*>(mean)[threadIdx.x] =
+          make_float4((float)((int)(even & 0xffffu) - kOff) * f, (float)((int)(odd & 0xffffu) - kOff) * f,
+                      (float)((int)(even >> 16) - kOff) * f, (float)((int)(odd >> 16) - kOff) * f);
+    }
+    return;
+  }
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     float x[4];
-    decode4<KIND>(reinterpret_cast<const uint32_t*>(tile + (p * R + r) * D)[w], x);
+    decode4<KIND>(word[r * W], x);
     s.x += x[0];
     s.y += x[1];
     s.z += x[2];
@@ -119,7 +145,6 @@ __device__ __forceinline__ void write_mean(const uint8_t* tile, float scale, flo
       s.z += y.z;
       s.w += y.w;
     }
-    const float f = scale * (1.f / kBlock);
     reinterpret_cast<float4*>(mean)[threadIdx.x] = make_float4(s.x * f, s.y * f, s.z * f, s.w * f);
   }
 }
@@ -239,12 +264,11 @@ __global__ void __launch_bounds__(kCta) append_kernel(const CacheView c, const _
 // weight and the first few equal to it. Each CTA keeps its eighth of the weights in shared
 // memory as integers of the same order. The threshold is found digit by digit, 8 bits at a
 // time: the CTAs' histograms are added through distributed shared memory. Weights crowd in
-// a few digits, so lanes with the same digit count together before the shared atomic. Then
+// few values of the first digit, so there lanes with the same one count together. Then
 // every CTA counts its run, takes its place from the counts of those before, and writes its
 // kept slots in order.
 // ---------------------------------------------------------------------------
 constexpr int kSelCluster = 8;
-constexpr int kSelThreads = 1024;
 
 __device__ __forceinline__ uint32_t weight_key(float w) {
   if (isnan(w)) w = -INFINITY;
@@ -269,17 +293,18 @@ __device__ __forceinline__ int peer_int(const int* p, uint32_t rank) {
 }
 
 // Slots of one CTA's run: a multiple of 32 a warp.
-__host__ __device__ inline int select_run(int n) {
-  return (int)align_up((size_t)(n + kSelCluster - 1) / kSelCluster, kSelThreads);
+__host__ __device__ inline int select_run(int n, int threads) {
+  return (int)align_up((size_t)(n + kSelCluster - 1) / kSelCluster, threads);
 }
 
+template <int kSelThreads>
 __global__ void __cluster_dims__(kSelCluster, 1, 1) __launch_bounds__(kSelThreads)
     evict_select_kernel(const CacheView c, const int32_t* __restrict__ lens, int budget, int n_sink, int n_recent,
                         int32_t* __restrict__ kept, int32_t* lens_out, int* __restrict__ flags, int n_flags) {
   extern __shared__ uint32_t keys[];  // [select_run(cap)]
   __shared__ int hist[2][256], total[256];
   __shared__ int s_digit, s_rest;
-  __shared__ int above[32], equal[32], mine[2];
+  __shared__ int above[kSelThreads / 32], equal[kSelThreads / 32], mine[2];
   const int bh = blockIdx.x / kSelCluster, b = bh / c.H_kv, hk = bh % c.H_kv;
   const int rank = (int)cluster_rank();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -299,7 +324,7 @@ __global__ void __cluster_dims__(kSelCluster, 1, 1) __launch_bounds__(kSelThread
     return;
   }
   const float* w = c.weight + (size_t)bh * c.cap;
-  const int run = select_run(n), a = min(n, rank * run), z = min(n, a + run);
+  const int run = select_run(n, kSelThreads), a = min(n, rank * run), z = min(n, a + run);
   const int lo = n_sink, hi = n - n_recent;    // n_sink + n_recent <= budget < n: lo < hi
   const int want = budget - n_sink - n_recent;  // of the slots between
   for (int i = a + tid; i < z; i += kSelThreads) keys[i - a] = weight_key(w[i]);
@@ -314,8 +339,12 @@ __global__ void __cluster_dims__(kSelCluster, 1, 1) __launch_bounds__(kSelThread
       for (int i = a + tid; i - lane < z; i += kSelThreads) {
         uint32_t dig = 256;
         if (i < z && i >= lo && i < hi && (keys[i - a] & mask) == prefix) dig = (keys[i - a] >> shift) & 255u;
-        const uint32_t same = __match_any_sync(0xffffffffu, dig);
-        if (dig < 256 && lane == __ffs(same) - 1) atomicAdd(&hist[turn][dig], __popc(same));
+        if (shift == 24) {  // sign and exponent: few digits
+          const uint32_t same = __match_any_sync(0xffffffffu, dig);
+          if (dig < 256 && lane == __ffs(same) - 1) atomicAdd(&hist[turn][dig], __popc(same));
+        } else if (dig < 256) {
+          atomicAdd(&hist[turn][dig], 1);
+        }
       }
       cluster_sync();
       if (tid < 256) {
@@ -359,7 +388,7 @@ __global__ void __cluster_dims__(kSelCluster, 1, 1) __launch_bounds__(kSelThread
     }
   }
   // keys above prefix stay, and the first `rest` equal to it (none of either where want is 0)
-  const int per = run / 32, wa = min(z, a + warp * per), wz = min(z, wa + per);
+  const int per = run / (kSelThreads / 32), wa = min(z, a + warp * per), wz = min(z, wa + per);
   int n_above = 0, n_equal = 0;
   for (int i = wa + lane; i - lane < wz; i += 32) {
     const bool held = i < wz && (i < lo || i >= hi), in = i < wz && !held && want > 0;
@@ -373,7 +402,9 @@ __global__ void __cluster_dims__(kSelCluster, 1, 1) __launch_bounds__(kSelThread
   }
   __syncthreads();
   if (warp == 0) {
-    const int x = __reduce_add_sync(0xffffffffu, above[lane]), y = __reduce_add_sync(0xffffffffu, equal[lane]);
+    const bool a_warp = lane < kSelThreads / 32;
+    const int x = __reduce_add_sync(0xffffffffu, a_warp ? above[lane] : 0);
+    const int y = __reduce_add_sync(0xffffffffu, a_warp ? equal[lane] : 0);
     if (lane == 0) {
       mine[0] = x;
       mine[1] = y;
@@ -481,13 +512,8 @@ __global__ void __launch_bounds__(kCta) evict_move_kernel(const CacheView c, con
   float ka = 0.f, va = 0.f;
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
-    float x[4];
-    decode4<KIND>(max_byte(__vmaxu4(__vmaxu4(abs4<KIND>(kc[i].x), abs4<KIND>(kc[i].y)),
-                                    __vmaxu4(abs4<KIND>(kc[i].z), abs4<KIND>(kc[i].w)))), x);
-    ka = fmaxf(ka, fabsf(x[0] * ks[i]));
-    decode4<KIND>(max_byte(__vmaxu4(__vmaxu4(abs4<KIND>(vc[i].x), abs4<KIND>(vc[i].y)),
-                                    __vmaxu4(abs4<KIND>(vc[i].z), abs4<KIND>(vc[i].w)))), x);
-    va = fmaxf(va, fabsf(x[0] * vs[i]));
+    ka = fmaxf(ka, max_magnitude16<KIND>(kc[i]) * ks[i]);
+    va = fmaxf(va, max_magnitude16<KIND>(vc[i]) * vs[i]);
   }
   const uint32_t kw = __reduce_max_sync(0xffffffffu, __float_as_uint(ka));
   const uint32_t vw = __reduce_max_sync(0xffffffffu, __float_as_uint(va));
@@ -613,12 +639,18 @@ sla_status sla_cache_evict(const sla_cache_config* cfg, const sla_cache* cache, 
   cudaStream_t s = (cudaStream_t)stream;
   int* flags = (int*)ws;
   const int n_flags = evict_flags(budget), nd = n_flags - 1;
-  const int smem = select_run(c.cap) * (int)sizeof(uint32_t);
-  if (cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           select_run(kMaxBlocks * kBlock) * (int)sizeof(uint32_t)) != cudaSuccess)
-    return SLA_ERR_CUDA;
-  evict_select_kernel<<<c.B * c.H_kv * kSelCluster, kSelThreads, smem, s>>>(c, lens, budget, n_sink, n_recent, kept,
-                                                                           lens_out, flags, n_flags);
+  // The keys take turns of one a thread: 1024 threads where all CTAs are resident at once with
+  // them (65536 slots of 4 heads: 31 us for the call, 35 with 512), else 512 (64 heads of 16384
+  // slots: 60 us, 72 with 1024, whose 512 CTAs came in two waves).
+  auto select = [&](auto kernel, int threads) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             select_run(kMaxBlocks * kBlock, threads) * (int)sizeof(uint32_t)) != cudaSuccess)
+      return;
+    kernel<<<c.B * c.H_kv * kSelCluster, threads, select_run(c.cap, threads) * (int)sizeof(uint32_t), s>>>(
+        c, lens, budget, n_sink, n_recent, kept, lens_out, flags, n_flags);
+  };
+  if (c.B * c.H_kv * kSelCluster <= 2 * 148) select(evict_select_kernel<1024>, 1024);
+  else select(evict_select_kernel<512>, 512);
   if (cudaGetLastError() != cudaSuccess) return SLA_ERR_CUDA;
   cudaLaunchConfig_t launch = {};
   launch.gridDim = dim3((unsigned)(c.B * c.H_kv * nd));

@@ -78,16 +78,6 @@ __device__ __forceinline__ void decode4_f16(uint32_t c, uint32_t& lo, uint32_t& 
   hi = *reinterpret_cast<const uint32_t*>(&y);
 }
 
-// largest code magnitude of four codes, as a code byte; e4m3 magnitudes order like integers
-template <int KIND>
-__device__ __forceinline__ uint32_t abs4(uint32_t c) {
-  return KIND == SLA_CACHE_E4M3 ? c & 0x7f7f7f7fu : __vabsss4(c);
-}
-__device__ __forceinline__ uint32_t max_byte(uint32_t c) {
-  c = __vmaxu4(c, c >> 16);
-  return max(c & 255u, (c >> 8) & 255u);
-}
-
 template <int KIND>
 __device__ __forceinline__ void decode4(uint32_t c, float* x) {
   uint32_t a, b;
@@ -98,6 +88,28 @@ __device__ __forceinline__ void decode4(uint32_t c, float* x) {
   x[1] = f.y;
   x[2] = g.x;
   x[3] = g.y;
+}
+
+// largest magnitude of 16 codes, by pairs of 16-bit lanes (e4m3 magnitudes order like integers)
+template <int KIND>
+__device__ __forceinline__ float max_magnitude16(const uint4& c) {
+  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+  uint32_t hi = 0, lo = 0x00ff00ffu;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t u = KIND == SLA_CACHE_E4M3 ? w[i] & 0x7f7f7f7fu : w[i] ^ 0x80808080u;
+    const uint32_t a = u & 0x00ff00ffu, b = (u >> 8) & 0x00ff00ffu;
+    hi = __vmaxu2(hi, __vmaxu2(a, b));
+    if (KIND == SLA_CACHE_INT8) lo = __vminu2(lo, __vminu2(a, b));
+  }
+  const int top = (int)max(hi & 0xffffu, hi >> 16);
+  if (KIND == SLA_CACHE_INT8) {
+    const int low = (int)min(lo & 0xffffu, lo >> 16);
+    return (float)max(top - 128, 128 - low);
+  }
+  float x[4];
+  decode4<KIND>((uint32_t)top, x);
+  return x[0];
 }
 
 // ---------------------------------------------------------------------------
