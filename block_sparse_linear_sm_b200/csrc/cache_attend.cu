@@ -26,141 +26,18 @@
 // movmatrix turns P's 8 x 8 pieces into the second product's operand.
 #include <cuda.h>
 
-#include "cache.cuh"
-#include "tc.cuh"
+#include "cache_attend.cuh"
 
 namespace sla {
 namespace {
+
+using namespace attend;
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kSlots = 2;       // pages in a warp's ring: keys and values of a tile
 constexpr int kCtasPerSm = 2;
-constexpr int kMinRun = kWarps;  // tiles a CTA takes at least
-constexpr float kShift = 15.f;
-
-struct Step {
-  const __nv_bfloat16* q;
-  const int32_t *lens, *n_new, *sel;
-  __nv_bfloat16* out;
-  float* part_ml;   // [slots][2][rows of a group]: m, l of a partial
-  float* part_o;    // [slots][rows of a group][D]
-  float* lse;       // [B, H, T] log2-sum-exp (with weights)
-  float* scores;    // [tiles of all (sequence, KV head)][64][score_rows] (with weights)
-  int T, top_n, window, rows, groups;  // rows = T * group of a KV head, in groups of 8 or 16
-  int score_rows;                      // rows rounded up to 8
-};
-
-// ---------------------------------------------------------------------------
-// the line of tiles
-// ---------------------------------------------------------------------------
-// Tiles of one (sequence, KV head): list entries first, then the window's (or all) blocks.
-__device__ __forceinline__ int first_block(const Step& a, int L, int n) {
-  return a.window > 0 ? max(0, L - n - a.window + 1) / kBlock : 0;
-}
-__device__ __forceinline__ int tile_count(const Step& a, int L, int n) {
-  if (n == 0 || L == 0) return 0;
-  const int range = (L + kBlock - 1) / kBlock - first_block(a, L, n);
-  return a.sel == nullptr ? range : a.top_n + (a.window > 0 ? range : 0);
-}
-
-struct Lines {  // in shared memory
-  int* cum;     // [B + 1]: tiles of one KV head of the sequences before
-  int* len;     // [B]
-  uint8_t* fresh;  // [B]: valid query rows of a head
-};
-__host__ __device__ inline size_t lines_bytes(int B) { return align_up((size_t)(2 * B + 1) * 4 + B, 16); }
-
-// All threads of the block; ends with a barrier.
-__device__ void scan_lines(const CacheView& c, const Step& a, char* smem, Lines* out, int* warp_sums) {
-  Lines l;
-  l.cum = reinterpret_cast<int*>(smem);
-  l.len = l.cum + c.B + 1;
-  l.fresh = reinterpret_cast<uint8_t*>(l.len + c.B);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
-  const int per = (c.B + blockDim.x - 1) / blockDim.x, b0 = tid * per;
-  int mine = 0;
-  for (int b = b0; b < min(c.B, b0 + per); ++b) {
-    bool bad = false;
-    const int L = checked_len(a.lens, b, c.cap, &bad), n = checked_new(a.n_new, b, a.T, &bad);
-    if (bad && blockIdx.x == 0) report(c.status, SLA_ERR_DEVICE_CHECK, kDetailCacheLen);
-    l.len[b] = L;
-    l.fresh[b] = (uint8_t)n;
-    const int t = tile_count(a, L, n);
-    l.cum[b] = t;
-    mine += t;
-  }
-  int upto = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, upto, o);
-    if (lane >= o) upto += y;
-  }
-  if (lane == 31) warp_sums[warp] = upto;
-  __syncthreads();
-  int before = upto - mine;
-  for (int w = 0; w < nw; ++w)
-    if (w < warp) before += warp_sums[w];
-  for (int b = b0; b < min(c.B, b0 + per); ++b) {
-    const int t = l.cum[b];
-    l.cum[b] = before;
-    before += t;
-  }
-  if (b0 < c.B && b0 + per >= c.B) l.cum[c.B] = before;
-  __syncthreads();
-  *out = l;
-}
-
-// Sequence that holds tile t of the line (per: segments a KV-head line of a sequence has).
-__device__ __forceinline__ int find_sequence(const Lines& l, int B, unsigned t, unsigned per) {
-  int lo = 0, hi = B - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if ((unsigned)l.cum[mid] * per <= t) lo = mid;
-    else hi = mid - 1;
-  }
-  // sequences without tiles share their number with the next: the last of them was found
-  return lo;
-}
-
-// Block of tile idx of (b, hk); -1 where it is none. *chosen: the window does not limit it.
-// Called by a whole warp.
-__device__ __forceinline__ int tile_block(const CacheView& c, const Step& a, int b, int hk, int idx, int L, int n,
-                                          int lane, bool* chosen) {
-  const int first = first_block(a, L, n);
-  if (a.sel == nullptr) {
-    *chosen = a.window == 0;
-    return first + idx;
-  }
-  const int32_t* list = a.sel + ((size_t)b * c.H_kv + hk) * a.top_n;
-  const int e0 = lane < a.top_n ? list[lane] : -1, e1 = lane + 32 < a.top_n ? list[lane + 32] : -1;
-  // an entry counts where it is above every earlier one and inside the sequence
-  int p0 = e0, p1 = e1;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y0 = __shfl_up_sync(0xffffffffu, p0, o), y1 = __shfl_up_sync(0xffffffffu, p1, o);
-    if (lane >= o) {
-      p0 = max(p0, y0);
-      p1 = max(p1, y1);
-    }
-  }
-  const int all0 = __shfl_sync(0xffffffffu, p0, 31);
-  int before0 = __shfl_up_sync(0xffffffffu, p0, 1), before1 = __shfl_up_sync(0xffffffffu, p1, 1);
-  if (lane == 0) before0 = before1 = -1;
-  before1 = max(before1, all0);
-  const int blocks = (L + kBlock - 1) / kBlock;
-  const bool ok0 = e0 >= 0 && e0 > before0 && e0 < blocks, ok1 = e1 >= 0 && e1 > before1 && e1 < blocks;
-  if (idx < a.top_n) {
-    *chosen = true;
-    const int e = __shfl_sync(0xffffffffu, idx < 32 ? e0 : e1, idx & 31);
-    const bool ok = __shfl_sync(0xffffffffu, (int)(idx < 32 ? ok0 : ok1), idx & 31) != 0;
-    if (!ok && e >= 0 && lane == 0) report(c.status, SLA_ERR_DEVICE_CHECK, kDetailCacheSel);
-    return ok ? e : -1;
-  }
-  *chosen = false;
-  const int j = first + idx - a.top_n;
-  return __any_sync(0xffffffffu, (ok0 && e0 == j) || (ok1 && e1 == j)) ? -1 : j;
-}
+constexpr int kFewRows = 16;    // more rows of a KV head go to the tcgen05 kernel
 
 // ---------------------------------------------------------------------------
 // instructions
@@ -171,22 +48,10 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
 __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
   uint32_t y;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
-}
-__device__ __forceinline__ void sts128(uint32_t addr, uint32_t x) {
-  asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(addr), "r"(x) : "memory");
-}
-__device__ __forceinline__ uint4 lds128(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
-  return v;
 }
 // Two 16 x 16 byte matrices, transposed: lane (g = lane / 4, q = lane % 4) gets in r[2 i]
 // rows 4 q .. 4 q + 3 of column g of matrix i and in r[2 i + 1] of column g + 8. Lanes
@@ -197,15 +62,6 @@ __device__ __forceinline__ void ldmatrix_trans_b8(uint32_t (&r)[4], uint32_t add
                : "r"(addr)
                : "memory");
 }
-__device__ __forceinline__ void tma_load_rows(uint32_t dst, const CUtensorMap* map, uint32_t bar, int row) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
-          dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(0), "r"(row)
-      : "memory");
-}
-__device__ __forceinline__ float log2_sum(float m, float l) { return l == 0.f ? -INFINITY : m + log2f(l); }
-
 // ---------------------------------------------------------------------------
 // a warp's ring
 // ---------------------------------------------------------------------------
@@ -314,21 +170,6 @@ struct Smem {
   static size_t bytes(int B) { return off_lines + lines_bytes(B); }
 };
 
-// A segment of the line: one row group of one KV head of one sequence, with its tiles.
-struct Segment {
-  int b, sr;         // sequence, number in it
-  unsigned lo, nb;   // first tile of the line, tiles
-};
-__device__ __forceinline__ void next_segment(Segment& s, const Lines& l, unsigned per) {
-  s.lo += s.nb;
-  if (++s.sr == (int)per) {
-    s.sr = 0;
-    do ++s.b;
-    while (l.cum[s.b + 1] == l.cum[s.b]);  // there is a tile ahead, so there is such a sequence
-    s.nb = l.cum[s.b + 1] - l.cum[s.b];
-  }
-}
-
 // NR: query rows of a segment in eights.
 template <int KIND, int D, int NR>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
@@ -365,7 +206,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 
   // this CTA's run of the line
   const unsigned per = c.H_kv * a.groups, total = (unsigned)l.cum[c.B] * per;
-  const unsigned run = max((total + gridDim.x - 1) / gridDim.x, (unsigned)kMinRun);
+  const unsigned run = max((total + gridDim.x - 1) / gridDim.x, a.min_run);
   const unsigned lo = min(total, blockIdx.x * run), hi = min(total, lo + run);
   if (lo >= hi) return;
 
@@ -726,7 +567,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const CacheView c, c
   Lines l;
   scan_lines(c, a, smem, &l, warp_sums);
   const unsigned per = c.H_kv * a.groups, total = (unsigned)l.cum[c.B] * per;
-  const unsigned run = max((total + ctas - 1) / ctas, (unsigned)kMinRun);
+  const unsigned run = max((total + ctas - 1) / ctas, a.min_run);
   const int seg = blockIdx.x, b = seg / (int)per, sr = seg % (int)per, hk = sr / a.groups;
   const int r = blockIdx.y * (W / PW) + warp / PW, row = sr % a.groups * rows + r;
   const int nb = l.cum[b + 1] - l.cum[b];
@@ -852,7 +693,7 @@ sla_status plan_step(const sla_cache_config* c, int32_t T, int32_t top_n, int32_
   const int64_t rows = (int64_t)T * (c->H / c->H_kv);
   if (T > kCacheMaxT || rows > kCacheMaxRows || top_n > kCacheMaxSel) return SLA_ERR_UNSUPPORTED;
   p->rows = (int)rows;
-  p->group_rows = p->rows <= 8 ? 8 : 16;
+  p->group_rows = p->rows <= 8 ? 8 : p->rows <= kFewRows ? 16 : kTcGroupRows;
   p->groups = (p->rows + p->group_rows - 1) / p->group_rows;
   const int64_t segs = (int64_t)c->B * c->H_kv * p->groups;
   const int64_t tiles = (int64_t)c->B * c->H_kv * most_tiles(c, T, top_n, window);
@@ -885,38 +726,51 @@ void launch_after(cudaLaunchConfig_t* cfg, dim3 grid, int threads, size_t smem, 
 }
 
 template <int KIND, int D, int NR>
-cudaError_t launch(const CacheView& c, const Step& a, int sms, cudaStream_t s) {
+cudaError_t launch(const CacheView& c, const Step& a, int ctas, cudaStream_t s) {
   CUtensorMap kmap, vmap;
   const uint64_t rows = (uint64_t)c.n_pages * c.H_kv * kBlock;
   if (!make_tmap_rows_u8(&kmap, c.k, rows, D, kBlock) || !make_tmap_rows_u8(&vmap, c.v, rows, D, kBlock))
     return cudaErrorInvalidValue;
   auto attend = attend_kernel<KIND, D, NR>;
-  cudaError_t e = cudaFuncSetAttribute(attend, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Smem<D, NR>::bytes(kCacheMaxB));
+  const cudaError_t e =
+      cudaFuncSetAttribute(attend, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Smem<D, NR>::bytes(kCacheMaxB));
   if (e != cudaSuccess) return e;
-  const int ctas = kCtasPerSm * sms < kMaxCtas ? kCtasPerSm * sms : kMaxCtas;
   attend<<<ctas, kThreads, Smem<D, NR>::bytes(c.B), s>>>(kmap, vmap, c, a);
-  e = cudaGetLastError();
+  return cudaGetLastError();
+}
+
+template <int KIND, int D>
+cudaError_t launch_rows(const CacheView& c, const Step& a, int ctas, cudaStream_t s) {
+  return a.group_rows == 8 ? launch<KIND, D, 1>(c, a, ctas, s) : launch<KIND, D, 2>(c, a, ctas, s);
+}
+
+cudaError_t launch_attend(const CacheView& c, const Step& a, int ctas, cudaStream_t s) {
+  if (a.group_rows == kTcGroupRows) return launch_attend_tc(c, a, ctas, s);
+  if (c.kind == SLA_CACHE_E4M3)
+    return c.d == 128 ? launch_rows<SLA_CACHE_E4M3, 128>(c, a, ctas, s) : launch_rows<SLA_CACHE_E4M3, 64>(c, a, ctas, s);
+  return c.d == 128 ? launch_rows<SLA_CACHE_INT8, 128>(c, a, ctas, s) : launch_rows<SLA_CACHE_INT8, 64>(c, a, ctas, s);
+}
+
+template <int D>
+cudaError_t launch_step(const CacheView& c, const Step& a, int sms, cudaStream_t s) {
+  const int per_sm = a.group_rows == kTcGroupRows ? 1 : kCtasPerSm;
+  const int ctas = per_sm * sms < kMaxCtas ? per_sm * sms : kMaxCtas;
+  cudaError_t e = launch_attend(c, a, ctas, s);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute at[1];
-  const int segs = c.B * c.H_kv * a.groups;
-  const int most = a.rows < 8 * NR ? a.rows : 8 * NR;
+  const int segs = c.B * c.H_kv * a.groups, most = a.rows < a.group_rows ? a.rows : a.group_rows;
   // A warp a row where segments are cut into few parts, eight where one is spread over the device
   if (ctas > 16 * segs) {
     launch_after(&cfg, dim3(segs, most), kJoinThreads, lines_bytes(c.B), s, at);
-    e = cudaLaunchKernelEx(&cfg, join_kernel<D, 8>, c, a, (unsigned)ctas, 8 * NR);
+    e = cudaLaunchKernelEx(&cfg, join_kernel<D, 8>, c, a, (unsigned)ctas, a.group_rows);
   } else {
     launch_after(&cfg, dim3(segs, (most + 7) / 8), kJoinThreads, lines_bytes(c.B), s, at);
-    e = cudaLaunchKernelEx(&cfg, join_kernel<D, 1>, c, a, (unsigned)ctas, 8 * NR);
+    e = cudaLaunchKernelEx(&cfg, join_kernel<D, 1>, c, a, (unsigned)ctas, a.group_rows);
   }
   if (e != cudaSuccess || c.weight == nullptr) return e;
   launch_after(&cfg, dim3(8 * sms), kThreads, lines_bytes(c.B), s, at);
   return cudaLaunchKernelEx(&cfg, weight_kernel, c, a);
-}
-
-template <int KIND, int D>
-cudaError_t launch_rows(const CacheView& c, const Step& a, int group_rows, int sms, cudaStream_t s) {
-  return group_rows == 8 ? launch<KIND, D, 1>(c, a, sms, s) : launch<KIND, D, 2>(c, a, sms, s);
 }
 
 }  // namespace
@@ -961,17 +815,13 @@ sla_status sla_cache_attend(const void* q, const sla_cache_config* cfg, const sl
   a.window = window < c.cap + kCacheMaxT ? window : c.cap + kCacheMaxT;  // more sees no more
   a.rows = p.rows;
   a.groups = p.groups;
+  a.group_rows = p.group_rows;
+  a.min_run = p.group_rows == kTcGroupRows ? 1 : kWarps;
   a.score_rows = (int)align_up(p.rows, 8);
   const int sms = sm_count();
   if (sms < 1) return SLA_ERR_CUDA;
   cudaStream_t s = (cudaStream_t)stream;
-  cudaError_t e;
-  if (c.kind == SLA_CACHE_E4M3)
-    e = c.d == 128 ? launch_rows<SLA_CACHE_E4M3, 128>(c, a, p.group_rows, sms, s)
-                   : launch_rows<SLA_CACHE_E4M3, 64>(c, a, p.group_rows, sms, s);
-  else
-    e = c.d == 128 ? launch_rows<SLA_CACHE_INT8, 128>(c, a, p.group_rows, sms, s)
-                   : launch_rows<SLA_CACHE_INT8, 64>(c, a, p.group_rows, sms, s);
+  const cudaError_t e = c.d == 128 ? launch_step<128>(c, a, sms, s) : launch_step<64>(c, a, sms, s);
   return e == cudaSuccess ? SLA_OK : SLA_ERR_CUDA;
 }
 

@@ -272,9 +272,9 @@ def test_attend_more_rows_than_tokens():
 
 
 @pytest.mark.parametrize("window", [1, 2, 63, 64, 65, 200, 100000])
-@pytest.mark.parametrize("T", [1, 5])
-def test_attend_window(window, T):
-    p = Pair(B=3, H=4, H_kv=2, d=64, max_blocks=8, kind=INT8, seed=window)
+@pytest.mark.parametrize("T,H", [(1, 4), (5, 4), (7, 20)])
+def test_attend_window(window, T, H):
+    p = Pair(B=3, H=H, H_kv=2, d=64, max_blocks=8, kind=INT8, seed=window)
     p.fill([500, 70, 6])
     p.check_attend(p.queries(T), window=window)
 
@@ -287,10 +287,10 @@ def lists(p, rows, top_n):
 
 
 @pytest.mark.parametrize("window", [0, 1, 70, 300])
-@pytest.mark.parametrize("T", [1, 4])
+@pytest.mark.parametrize("T,H", [(1, 8), (4, 8), (5, 32)])
 @pytest.mark.parametrize("kind", [E4M3, INT8])
-def test_attend_selected_blocks(window, T, kind):
-    p = Pair(B=3, H=8, H_kv=2, d=128, max_blocks=12, kind=kind, seed=window + T)
+def test_attend_selected_blocks(window, T, H, kind):
+    p = Pair(B=3, H=H, H_kv=2, d=128, max_blocks=12, kind=kind, seed=window + T)
     p.fill([700, 130, 20])
     # ragged lists, an empty one, blocks that the window holds too, the open block itself
     sel = lists(p, {(0, 0): [0, 3, 9], (0, 1): [1, 2, 4, 6, 10], (1, 0): [0], (1, 1): [0, 1, 2]}, 5)
@@ -300,14 +300,16 @@ def test_attend_selected_blocks(window, T, kind):
         assert not out[2].any()   # no block, no window
 
 
-def test_attend_longest_list():
-    p = Pair(B=1, H=4, H_kv=1, d=64, max_blocks=70, seed=9)
+@pytest.mark.parametrize("T,H", [(1, 4), (6, 8)])
+def test_attend_longest_list(T, H):
+    p = Pair(B=1, H=H, H_kv=1, d=64, max_blocks=70, seed=9)
     p.fill([70 * 64])
-    p.check_attend(p.queries(1), sel=lists(p, {(0, 0): list(range(3, 67))}, 64), window=65)
+    p.check_attend(p.queries(T), sel=lists(p, {(0, 0): list(range(3, 67))}, 64), window=65)
 
 
-def test_attend_reports_bad_lists_pages_and_lengths():
-    p = Pair(B=2, H=4, H_kv=2, d=64, max_blocks=6, seed=10)
+@pytest.mark.parametrize("H", [4, 96])
+def test_attend_reports_bad_lists_pages_and_lengths(H):
+    p = Pair(B=2, H=H, H_kv=2, d=64, max_blocks=6, seed=10)
     p.fill([300, 200])
     q = p.queries(1)
     good = lists(p, {(0, 0): [1, 3], (0, 1): [2], (1, 0): [0, 2]}, 3)
@@ -341,21 +343,27 @@ def test_attend_reports_bad_lists_pages_and_lengths():
     assert not out[1].any() and out[0].any()
 
 
-def test_attend_large_scores_and_one_hot_rows():
+@pytest.mark.parametrize("H", [4, 40])
+def test_attend_large_scores_and_one_hot_rows(H):
     """Scores of some hundred: one token takes all; no overflow, no NaN."""
-    p = Pair(B=1, H=4, H_kv=1, d=128, max_blocks=6, kind=INT8, seed=11)
+    p = Pair(B=1, H=H, H_kv=1, d=128, max_blocks=6, kind=INT8, seed=11)
     p.fill([333], std=8.0)
     q = p.queries(1, std=100.0)
     out = p.attend(q)
     want, mag, _ = p.o.attend(f64(q), p.lens, [1], None, 0)
     # scores near 2^14 have errors up to 2^14 * 2^-22 = 2^-8 absolute where tokens compete
-    assert np.all(np.abs(f64(out) - want) <= (2.0 ** -8 + 2.0 ** -7) * mag + 1e-30)
+    # a weight is held as fp16 of 2^15 times it: its step is 2^-24 / 2^15 at least, so each of
+    # the 333 is off by up to half of that, 2^-40, and one below it counts as 0. Where the one
+    # token that takes all has value 0 in a column, that is all there is
+    floor = 333 * 2.0 ** -40 * np.abs(p.o.rows(0, 0, 333)[1]).max()
+    assert np.all(np.abs(f64(out) - want) <= (2.0 ** -8 + 2.0 ** -7) * mag + floor)
 
 
 @pytest.mark.parametrize("lo,hi", [(-100, -90), (-60, 60), (90, 110)])
-def test_attend_scales_far_apart(lo, hi):
+@pytest.mark.parametrize("H", [4, 33])
+def test_attend_scales_far_apart(lo, hi, H):
     """Pages whose value scales differ by many binades, and tiny or huge values."""
-    p = Pair(B=1, H=4, H_kv=1, d=64, max_blocks=4, kind=E4M3, seed=12)
+    p = Pair(B=1, H=H, H_kv=1, d=64, max_blocks=4, kind=E4M3, seed=12)
     for j, e in enumerate((lo, hi, lo)):
         k, v = p.kv(64)
         p.append(k, (v.float() * 2.0 ** e).bfloat16())
@@ -367,9 +375,10 @@ def test_attend_scales_far_apart(lo, hi):
 
 
 @pytest.mark.parametrize("std", [2.0 ** -40, 2.0 ** 40])
-def test_attend_query_magnitudes(std):
+@pytest.mark.parametrize("H", [4, 60])
+def test_attend_query_magnitudes(std, H):
     """Tiny queries give equal weights; huge ones one token's value. Rows differ in magnitude."""
-    p = Pair(B=1, H=4, H_kv=2, d=64, max_blocks=3, seed=13)
+    p = Pair(B=1, H=H, H_kv=2, d=64, max_blocks=3, seed=13)
     p.fill([150])
     q = p.queries(1)
     q[0, 1] = (q[0, 1].float() * std).bfloat16()
@@ -377,19 +386,19 @@ def test_attend_query_magnitudes(std):
     out = p.attend(q, weight=False)
     want, mag, _ = p.o.attend(f64(q), p.lens, [1], None, 0)
     tol = 2.0 ** -8 * np.abs(want) + (2.0 ** -11 + 2.0 ** -16) * mag
-    rows = [0, 1, 2, 3]
-    assert np.all(np.abs(f64(out) - want)[:, rows] <= tol[:, rows])
+    assert np.all(np.abs(f64(out) - want) <= tol)
 
 
-def test_attend_nan_query_stays_in_its_row():
-    p = Pair(B=2, H=8, H_kv=2, d=64, seed=14)
+@pytest.mark.parametrize("H", [8, 24])
+def test_attend_nan_query_stays_in_its_row(H):
+    p = Pair(B=2, H=H, H_kv=2, d=64, seed=14)
     p.fill([100, 100])
     q = p.queries(2)
     want = p.attend(q, weight=False)
     q2 = q.clone()
     q2[0, 3, 1, 5], q2[1, 6, 0, 2] = float("nan"), float("inf")
     out = p.attend(q2, weight=False)
-    rest = torch.ones(2, 8, 2, dtype=torch.bool)
+    rest = torch.ones(2, H, 2, dtype=torch.bool)
     rest[0, 3, 1] = rest[1, 6, 0] = False
     assert torch.equal(out[rest], want[rest])
     assert torch.isnan(out[0, 3, 1]).all() and torch.isnan(out[1, 6, 0]).all()
@@ -406,10 +415,16 @@ def test_attend_shared_pages():
     p.check_attend(p.queries(1))
 
 
-def test_attend_many_sequences_and_group_sizes():
-    p = Pair(B=300, H=3, H_kv=3, d=64, max_blocks=2, kind=INT8, seed=16)
+@pytest.mark.parametrize("H,T", [(3, 1), (9, 7)])
+def test_attend_many_sequences(H, T):
+    p = Pair(B=300, H=H, H_kv=3, d=64, max_blocks=2, kind=INT8, seed=16)
     p.fill(np.arange(300) % 128)
-    p.check_attend(p.queries(1))
+    p.check_attend(p.queries(T))
+    # most lists empty: many neighbouring segments without a page
+    sel = np.full((300, 3, 2), -1)
+    sel[::37, 1, 0] = 0
+    sel[p.lens == 0] = -1
+    p.check_attend(p.queries(T), sel=sel)
 
 
 def test_attend_many_rows():
@@ -419,10 +434,11 @@ def test_attend_many_rows():
     p.check_attend(p.queries(64))
 
 
-def test_attend_writes_the_same_bits_again():
+@pytest.mark.parametrize("T", [2, 5])
+def test_attend_writes_the_same_bits_again(T):
     p = Pair(B=4, H=16, H_kv=2, d=128, max_blocks=40, seed=18)
     p.fill([2500, 1, 700, 1300])
-    q = p.queries(2)
+    q = p.queries(T)
     p.c.weight.zero_()
     a = p.attend(q)
     w = p.c.weight.clone()
