@@ -526,12 +526,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         y.w += x.w;
       }
       const float top = mi.top[r], all = mi.all[r];
+      if (d4 == 0 && (!whole || a.scores != nullptr)) {
+        a.part_ml[part * 2 * kRows + r] = top;
+        a.part_ml[part * 2 * kRows + kRows + r] = all;
+      }
       if (!whole) {
         reinterpret_cast<float4*>(a.part_o)[part * (kRows * D / 4) + e] = y;
-        if (d4 == 0) {
-          a.part_ml[part * 2 * kRows + r] = top;
-          a.part_ml[part * 2 * kRows + kRows + r] = all;
-        }
       } else if (row0 + r < a.rows) {
         const bool empty = all == 0.f || (row0 + r) % a.T >= n;
         const float inv = 1.f / all;
@@ -552,13 +552,84 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 }
 
 // ---------------------------------------------------------------------------
+// weights: weight[b, hk, s] += sum over rows of 2^(score - lse), rows in order
+// ---------------------------------------------------------------------------
+// Warp `first` of `step`: a warp a tile (list entries that name no block are passed over), a
+// lane two slots. lse: this warp's log2-sum-exp of the tile's rows, put together from the
+// parts of its segments (run: tiles of a part); null: a.lse has them.
+__device__ void weigh(const CacheView& c, const Step& a, const Lines& l, unsigned first, unsigned step, int lane,
+                      float* lse, unsigned run) {
+  const unsigned per = c.H_kv, total = (unsigned)l.cum[c.B] * per;
+  int have = -1;  // (sequence, KV head) whose rows lse holds
+  for (unsigned t = first; t < total; t += step) {
+    const int b = find_sequence(l, c.B, t, per), nb = l.cum[b + 1] - l.cum[b], L = l.len[b], n = l.fresh[b];
+    const unsigned in = t - (unsigned)l.cum[b] * per;
+    const int hk = (int)(in / (unsigned)nb);
+    bool chosen;
+    const int j = tile_block(c, a, b, hk, (int)(in - (unsigned)hk * nb), L, n, lane, &chosen);
+    if (j < 0) continue;
+    const int page = c.table[(size_t)b * c.max_blocks + j];
+    if (page < 0 || page >= c.n_pages) continue;  // reported by the attention kernel
+    const float* row_lse = lse != nullptr ? lse : a.lse + ((size_t)b * c.H + (size_t)hk * c.group) * a.T;
+    if (lse != nullptr && have != b * c.H_kv + hk) {
+      have = b * c.H_kv + hk;
+      __syncwarp();
+      for (int r = lane; r < a.rows; r += 32) {
+        const int grp = r / a.group_rows, seg = have * a.groups + grp, at = r - grp * a.group_rows;
+        const unsigned lo = (unsigned)l.cum[b] * per * a.groups + (unsigned)(hk * a.groups + grp) * nb;
+        float m = -INFINITY, sum = 0.f;
+#pragma unroll 4
+        for (unsigned i = lo / run; i <= (lo + nb - 1) / run; ++i) {
+          const float* ml = a.part_ml + ((size_t)i + seg) * 2 * a.group_rows + at;
+          const float x = ml[0], y = ml[a.group_rows], next = fmaxf(m, x), base = next == -INFINITY ? 0.f : next;
+          sum = sum * tc::ex2_approx(m - base) + y * tc::ex2_approx(x - base);
+          m = next;
+        }
+        lse[r] = log2_sum(m, sum);
+      }
+      __syncwarp();
+    }
+    const float4* s = reinterpret_cast<const float4*>(a.scores + ((size_t)t * kBlock + lane) * a.score_rows);
+    const int half = 32 * a.score_rows / 4;  // from slot lane to slot lane + 32
+    float x = 0.f, y = 0.f;
+    for (int r = 0; r < a.rows; r += 4) {
+      const float4 u = s[r / 4], v = s[r / 4 + half];
+      const float us[4] = {u.x, u.y, u.z, u.w}, vs[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float z = r + e < a.rows && (a.T == 1 || (r + e) % a.T < n) ? row_lse[r + e] : -INFINITY;
+        if (z != -INFINITY) {
+          x += tc::ex2_approx(us[e] - z);
+          y += tc::ex2_approx(vs[e] - z);
+        }
+      }
+    }
+    float* w = c.weight + ((size_t)b * c.H_kv + hk) * c.cap + j * kBlock + lane;
+    if (j * kBlock + lane < L) *w += x;
+    if (j * kBlock + lane + 32 < L) w[32] += y;
+  }
+}
+
+// By itself: behind join_kernel, which has left lse.
+__global__ void __launch_bounds__(kThreads) weight_kernel(const CacheView c, const Step a) {
+  extern __shared__ __align__(1024) char smem[];
+  __shared__ int warp_sums[kWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  Lines l;
+  scan_lines(c, a, smem, &l, warp_sums);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  weigh(c, a, l, blockIdx.x * kWarps + warp, gridDim.x * kWarps, lane, nullptr, 0);
+}
+
+// ---------------------------------------------------------------------------
 // segments that several CTAs worked on, or none
 // ---------------------------------------------------------------------------
-// PW warps a row take the partials in turn, a lane D / 32 columns; a CTA has 8 / PW rows.
+// PW warps a row take the partials in turn, a lane D / 32 columns; a CTA has 8 / PW rows. CTAs
+// behind the segments' add the weights meanwhile.
 constexpr int kJoinThreads = 256;
 
 template <int D, int PW>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const CacheView c, const Step a, unsigned ctas, int rows) {
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const CacheView c, const Step a, unsigned ctas, int segs) {
   constexpr int E = D / 32, W = kJoinThreads / 32;
   extern __shared__ __align__(1024) char smem[];
   __shared__ int warp_sums[W];
@@ -568,7 +639,13 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const CacheView c, c
   scan_lines(c, a, smem, &l, warp_sums);
   const unsigned per = c.H_kv * a.groups, total = (unsigned)l.cum[c.B] * per;
   const unsigned run = max((total + ctas - 1) / ctas, a.min_run);
-  const int seg = blockIdx.x, b = seg / (int)per, sr = seg % (int)per, hk = sr / a.groups;
+  if (blockIdx.x >= segs) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    weigh(c, a, l, ((blockIdx.x - segs) * gridDim.y + blockIdx.y) * W + warp, (gridDim.x - segs) * gridDim.y * W, lane,
+          reinterpret_cast<float*>(smem + lines_bytes(c.B)) + warp * a.rows, run);
+    return;
+  }
+  const int rows = a.group_rows, seg = blockIdx.x, b = seg / (int)per, sr = seg % (int)per, hk = sr / a.groups;
   const int r = blockIdx.y * (W / PW) + warp / PW, row = sr % a.groups * rows + r;
   const int nb = l.cum[b + 1] - l.cum[b];
   const unsigned lo = (unsigned)l.cum[b] * per + (unsigned)sr * nb, hi = lo + nb;
@@ -617,49 +694,6 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const CacheView c, c
   for (int e = 0; e < E; e += 2)
     *reinterpret_cast<uint32_t*>(a.out + qrow * D + lane * E + e) = valid ? pack_bf16(o[e] / sum, o[e + 1] / sum) : 0u;
   if (lane == 0 && a.lse != nullptr) a.lse[qrow] = log2_sum(m, sum);
-}
-
-// ---------------------------------------------------------------------------
-// weights: weight[b, hk, s] += sum over rows of 2^(score - lse), rows in order
-// ---------------------------------------------------------------------------
-// A warp a tile (list entries that name no block are passed over), a lane two slots.
-__global__ void __launch_bounds__(kThreads) weight_kernel(const CacheView c, const Step a) {
-  extern __shared__ __align__(1024) char smem[];
-  __shared__ int warp_sums[kWarps];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  Lines l;
-  scan_lines(c, a, smem, &l, warp_sums);
-  const unsigned per = c.H_kv, total = (unsigned)l.cum[c.B] * per;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  for (unsigned t = blockIdx.x * kWarps + warp; t < total; t += gridDim.x * kWarps) {
-    const int b = find_sequence(l, c.B, t, per), nb = l.cum[b + 1] - l.cum[b], L = l.len[b], n = l.fresh[b];
-    const unsigned in = t - (unsigned)l.cum[b] * per;
-    const int hk = (int)(in / (unsigned)nb);
-    bool chosen;
-    const int j = tile_block(c, a, b, hk, (int)(in - (unsigned)hk * nb), L, n, lane, &chosen);
-    if (j < 0) continue;
-    const int page = c.table[(size_t)b * c.max_blocks + j];
-    if (page < 0 || page >= c.n_pages) continue;  // reported by the attention kernel
-    const float* lse = a.lse + ((size_t)b * c.H + (size_t)hk * c.group) * a.T;
-    const float4* s = reinterpret_cast<const float4*>(a.scores + ((size_t)t * kBlock + lane) * a.score_rows);
-    const int half = 32 * a.score_rows / 4;  // from slot lane to slot lane + 32
-    float x = 0.f, y = 0.f;
-    for (int r = 0; r < a.rows; r += 4) {
-      const float4 u = s[r / 4], v = s[r / 4 + half];
-      const float us[4] = {u.x, u.y, u.z, u.w}, vs[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float z = r + e < a.rows && (r + e) % a.T < n ? lse[r + e] : -INFINITY;
-        if (z != -INFINITY) {
-          x += tc::ex2_approx(us[e] - z);
-          y += tc::ex2_approx(vs[e] - z);
-        }
-      }
-    }
-    float* w = c.weight + ((size_t)b * c.H_kv + hk) * c.cap + j * kBlock + lane;
-    if (j * kBlock + lane < L) *w += x;
-    if (j * kBlock + lane + 32 < L) w[32] += y;
-  }
 }
 
 // ---------------------------------------------------------------------------
@@ -760,17 +794,20 @@ cudaError_t launch_step(const CacheView& c, const Step& a, int sms, cudaStream_t
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute at[1];
   const int segs = c.B * c.H_kv * a.groups, most = a.rows < a.group_rows ? a.rows : a.group_rows;
-  // A warp a row where segments are cut into few parts, eight where one is spread over the device
+  // A warp a row where segments are cut into few parts, eight where one is spread over the
+  // device. In the first case the weights' warps can put the parts' sums together themselves and
+  // run beside the join; in the second they would each read hundreds of parts.
   if (ctas > 16 * segs) {
     launch_after(&cfg, dim3(segs, most), kJoinThreads, lines_bytes(c.B), s, at);
-    e = cudaLaunchKernelEx(&cfg, join_kernel<D, 8>, c, a, (unsigned)ctas, a.group_rows);
-  } else {
-    launch_after(&cfg, dim3(segs, (most + 7) / 8), kJoinThreads, lines_bytes(c.B), s, at);
-    e = cudaLaunchKernelEx(&cfg, join_kernel<D, 1>, c, a, (unsigned)ctas, a.group_rows);
+    e = cudaLaunchKernelEx(&cfg, join_kernel<D, 8>, c, a, (unsigned)ctas, segs);
+    if (e != cudaSuccess || c.weight == nullptr) return e;
+    launch_after(&cfg, dim3(8 * sms), kThreads, lines_bytes(c.B), s, at);
+    return cudaLaunchKernelEx(&cfg, weight_kernel, c, a);
   }
-  if (e != cudaSuccess || c.weight == nullptr) return e;
-  launch_after(&cfg, dim3(8 * sms), kThreads, lines_bytes(c.B), s, at);
-  return cudaLaunchKernelEx(&cfg, weight_kernel, c, a);
+  const int y = (most + 7) / 8, more = c.weight != nullptr ? (4 * sms + y - 1) / y : 0;
+  const size_t smem = lines_bytes(c.B) + (c.weight != nullptr ? kJoinThreads / 32 * a.rows * sizeof(float) : 0);
+  launch_after(&cfg, dim3(segs + more, y), kJoinThreads, smem, s, at);
+  return cudaLaunchKernelEx(&cfg, join_kernel<D, 1>, c, a, (unsigned)ctas, segs);
 }
 
 }  // namespace

@@ -10,13 +10,14 @@
 //                   read, K [slot][d] and V [slot][d] (N-major), 128-byte swizzle;
 //   warp 1          issues S = Q K^T (M 128, N 64) and, one page behind, P V (M 128, N d) with
 //                   P as the operand in TMEM;
-//   warps 4 - 7     own a row a thread: maximum, P = 2^(S - m + 15) as fp16 back to TMEM, and
-//                   O = O 2^(m' - m) + 2^-15 v_scale * (P V) in fp32 registers.
+//   warps 4 - 7     own a row a thread: maximum, P = 2^(S - m + 8) as fp16 back to TMEM, and, a
+//                   page behind, O = O + 2^-8 v_scale * (P V) in fp32 registers.
 // Each page's P V goes to a buffer of its own (two, in turn) instead of accumulating in TMEM:
 // pages have value scales of their own, and with O in registers neither they nor a new maximum
-// need a pass over TMEM.
-// Q is scaled as in the kernel for few rows. S and P are double buffered, so that the softmax
-// of one page runs while the products of the next are issued.
+// need a pass over TMEM. m is raised, and O scaled, only when a maximum exceeds it by 2^7, so
+// that P stays below 2^15; a weight below 2^-33 of m's may round to 0. Q is scaled as in the
+// kernel for few rows. S and P are double buffered, so that the softmax of one page runs while
+// the products of the next are issued.
 #include "cache_attend.cuh"
 
 namespace sla {
@@ -27,8 +28,9 @@ using namespace attend;
 constexpr int kThreads = 384;
 constexpr int kRaw = 4;     // pages of codes in flight, keys and values together
 constexpr int kInfo = 16;   // described tiles
+constexpr float kTcShift = 8.f, kTcSlack = 7.f;
 
-struct Info {
+struct __align__(16) Info {
   int seg;      // segment of the line, -1: the run is over
   int real;     // 0: the segment has no page in this run (seg only)
   int block, tile, chosen, live;  // live: slots that hold tokens
@@ -49,7 +51,7 @@ struct Smem {
   static size_t bytes(int B) { return off_lines + lines_bytes(B); }
 };
 
-struct Misc {
+struct __align__(16) Misc {
   uint64_t raw_full[kRaw], raw_empty[kRaw];
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
   uint64_t s_full[2], s_empty[2], p_full[2], o_full[2], o_empty[2];
@@ -83,7 +85,16 @@ __device__ __forceinline__ void arrive_warp(uint64_t* bar, int lane) {
 // Reads entry e; every reader's warps give it back.
 __device__ __forceinline__ bool read_info(Misc& mi, unsigned e, int lane, Info* out) {
   if (!wait_all(&mi.info_full[e % kInfo], e / kInfo, mi)) return false;
-  *out = mi.info[e % kInfo];
+  const int4* p = reinterpret_cast<const int4*>(&mi.info[e % kInfo]);
+  const int4 x = p[0], y = p[1];
+  out->seg = x.x;
+  out->real = x.y;
+  out->block = x.z;
+  out->tile = x.w;
+  out->chosen = y.x;
+  out->live = y.y;
+  out->ks = __int_as_float(y.z);
+  out->vs = __int_as_float(y.w);
   arrive_warp(&mi.info_empty[e % kInfo], lane);
   return true;
 }
@@ -270,29 +281,38 @@ __device__ bool multiply(Misc& mi, char* smem, uint32_t tmem, int lane) {
 template <int KIND, int D>
 __device__ __forceinline__ void decode_page(uint32_t src, uint32_t dst, int tid, int live) {
   constexpr int kTurns = D / 64;  // chunk halves of a row
+  constexpr int kLanes = 128, kAll = 256 / kLanes * kTurns, kBatch = kAll < 4 ? kAll : 4;
 #pragma unroll
-  for (int i = 0; i < 2 * kTurns; ++i) {
-    const int o = (tid + 128 * (i / kTurns)) >> 3, w = tid & 7, turn = i % kTurns;
-    const int row = 2 * o + (w >> 2);
-    const int ch = D == 128 ? (w & 3) + 4 * (turn ^ (w >> 2)) : w & 3;
-    const uint4 x = lds128(src + row * D + ((ch ^ (D == 128 ? (row & 7) : ((row >> 1) & 3))) << 4));
-    uint32_t h[8];
-    decode4_f16<KIND>(x.x, h[0], h[1]);
-    decode4_f16<KIND>(x.y, h[2], h[3]);
-    decode4_f16<KIND>(x.z, h[4], h[5]);
-    decode4_f16<KIND>(x.w, h[6], h[7]);
-    if (row >= live) {
+  for (int i0 = 0; i0 < kAll; i0 += kBatch) {
+    uint4 x[kBatch];
+    int row[kBatch], ch[kBatch];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) h[e] = 0u;
+    for (int k = 0; k < kBatch; ++k) {  // the loads of a batch together: each is waited for once
+      const int i = i0 + k, o = (tid + kLanes * (i / kTurns)) >> 3, w = tid & 7, turn = i % kTurns;
+      row[k] = 2 * o + (w >> 2);
+      ch[k] = D == 128 ? (w & 3) + 4 * (turn ^ (w >> 2)) : w & 3;
+      x[k] = lds128(src + row[k] * D + ((ch[k] ^ (D == 128 ? (row[k] & 7) : ((row[k] >> 1) & 3))) << 4));
     }
-    const uint32_t at = dst + (ch >> 2) * 8192 + row * 128;
-    const int c16 = 2 * (ch & 3);
-    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at + ((c16 ^ (row & 7)) << 4)), "r"(h[0]), "r"(h[1]),
-                 "r"(h[2]), "r"(h[3])
-                 : "memory");
-    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at + (((c16 + 1) ^ (row & 7)) << 4)), "r"(h[4]),
-                 "r"(h[5]), "r"(h[6]), "r"(h[7])
-                 : "memory");
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      uint32_t h[8];
+      decode4_f16<KIND>(x[k].x, h[0], h[1]);
+      decode4_f16<KIND>(x[k].y, h[2], h[3]);
+      decode4_f16<KIND>(x[k].z, h[4], h[5]);
+      decode4_f16<KIND>(x[k].w, h[6], h[7]);
+      if (live < kBlock && row[k] >= live) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[e] = 0u;
+      }
+      const uint32_t at = dst + (ch[k] >> 2) * 8192 + row[k] * 128;
+      const int c16 = 2 * (ch[k] & 3);
+      asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at + ((c16 ^ (row[k] & 7)) << 4)), "r"(h[0]),
+                   "r"(h[1]), "r"(h[2]), "r"(h[3])
+                   : "memory");
+      asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at + (((c16 + 1) ^ (row[k] & 7)) << 4)), "r"(h[4]),
+                   "r"(h[5]), "r"(h[6]), "r"(h[7])
+                   : "memory");
+    }
   }
 }
 
@@ -344,13 +364,17 @@ __device__ bool rows_of_step(const CacheView& c, const Step& a, const Lines& l, 
     tc::fence_after_sync();
     const uint64_t v2 = tc::f2_pack(owed_vs, owed_vs);
 #pragma unroll
-    for (int u = 0; u < D / 32; ++u) {
-      uint32_t x[32];
-      tc::tmem_ld32(lanes + Cols<D>::acc + k * D + 32 * u, x);
+    for (int u = 0; u < D / 64; ++u) {
+      uint32_t x[32], y[32];
+      tc::tmem_ld32(lanes + Cols<D>::acc + k * D + 64 * u, x);
+      tc::tmem_ld32(lanes + Cols<D>::acc + k * D + 64 * u + 32, y);
       tc::tmem_ld_wait();
 #pragma unroll
-      for (int i2 = 0; i2 < 16; ++i2)
-        o[16 * u + i2] = tc::ffma2(v2, (uint64_t)x[2 * i2] | ((uint64_t)x[2 * i2 + 1] << 32), o[16 * u + i2]);
+      for (int i2 = 0; i2 < 16; ++i2) {
+        o[32 * u + i2] = tc::ffma2(v2, (uint64_t)x[2 * i2] | ((uint64_t)x[2 * i2 + 1] << 32), o[32 * u + i2]);
+        o[32 * u + 16 + i2] =
+            tc::ffma2(v2, (uint64_t)y[2 * i2] | ((uint64_t)y[2 * i2 + 1] << 32), o[32 * u + 16 + i2]);
+      }
     }
     tc::fence_before_sync();
     arrive_warp(&mi.o_empty[k], lane);
@@ -366,8 +390,14 @@ __device__ bool rows_of_step(const CacheView& c, const Step& a, const Lines& l, 
       if (seg >= 0) {
         const int sr = seg % (int)per, nb = l.cum[b + 1] - l.cum[b];
         const unsigned seg_lo = (unsigned)l.cum[b] * per + (unsigned)sr * nb;
-        const float all = sum * exp2_int(-(int)kShift);
-        if (seg_lo >= lo && seg_lo + nb <= hi) {
+        const float all = sum * exp2_int(-(int)kTcShift);
+        const bool whole = seg_lo >= lo && seg_lo + nb <= hi;
+        const size_t part = (size_t)blockIdx.x + seg;
+        if (!whole || a.scores != nullptr) {
+          a.part_ml[part * 2 * kTcGroupRows + r] = m;
+          a.part_ml[part * 2 * kTcGroupRows + kTcGroupRows + r] = all;
+        }
+        if (whole) {
           if (row < a.rows) {
             const bool empty = all == 0.f || pos < 0;
             const float inv = 1.f / all;
@@ -383,9 +413,6 @@ __device__ bool rows_of_step(const CacheView& c, const Step& a, const Lines& l, 
             if (a.lse != nullptr) a.lse[qrow] = log2_sum(m, all);
           }
         } else {
-          const size_t part = (size_t)blockIdx.x + seg;
-          a.part_ml[part * 2 * kTcGroupRows + r] = m;
-          a.part_ml[part * 2 * kTcGroupRows + kTcGroupRows + r] = all;
           ulonglong2* out = reinterpret_cast<ulonglong2*>(a.part_o + (part * kTcGroupRows + r) * D);
 #pragma unroll
           for (int u = 0; u < D / 4; ++u) out[u] = make_ulonglong2(o[2 * u], o[2 * u + 1]);
@@ -477,11 +504,15 @@ __device__ bool rows_of_step(const CacheView& c, const Step& a, const Lines& l, 
 #pragma unroll
       for (int u = 0; u < 4; ++u) mx[u] = i + 4 + u < 64 ? tc::fmax3(mx[u], s[i + u], s[i + 4 + u]) : fmaxf(mx[u], s[i + u]);
     const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-    const float low = top == -INFINITY ? 0.f : top, scaled = __fmul_rn(top, f), next = fmaxf(m, scaled);
-    const float base = next == -INFINITY ? 0.f : next;
-    const float off = (scaled == -INFINITY ? 0.f : scaled - base) + kShift;
-    const float alpha = tc::ex2_approx(m - base);
-    m = next;
+    // x = (s - page's maximum) * f + (its scaled value - m) + shift, with m raised first where
+    // the value exceeds it by the slack
+    const float low = top == -INFINITY ? 0.f : top, scaled = __fmul_rn(top, f);
+    const bool raise = scaled > m + kTcSlack;
+    const float alpha = raise ? tc::ex2_approx(m - scaled) : 1.f;
+    const bool any_raise = __any_sync(0xffffffffu, raise);
+    m = raise ? scaled : m;
+    sum *= alpha;
+    const float off = (scaled == -INFINITY ? 0.f : scaled - (m == -INFINITY ? 0.f : m)) + kTcShift;
     const uint64_t f2 = tc::f2_pack(f, f), l2 = tc::f2_pack(low, low), o2 = tc::f2_pack(off, off);
     uint32_t pk[32];
     uint64_t s2[2] = {0ull, 0ull};
@@ -493,20 +524,20 @@ __device__ bool rows_of_step(const CacheView& c, const Step& a, const Lines& l, 
       pk[i] = pack_f16(p0, p1);
     }
     s2[0] = tc::fadd2(s2[0], s2[1]);
-    sum = sum * alpha + (tc::f2_lo(s2[0]) + tc::f2_hi(s2[0]));
+    sum += tc::f2_lo(s2[0]) + tc::f2_hi(s2[0]);
     // this buffer's P was read by the product that was collected a page ago
     tc::tmem_st32(lanes + Cols<D>::p + 32 * k, pk);
     tc::tmem_st_wait();
     tc::fence_before_sync();
     arrive_warp(&mi.p_full[k], lane);
     if (owed && !collect(page - 1)) return false;
-    if (__any_sync(0xffffffffu, alpha != 1.f)) {
+    if (any_raise) {
       const uint64_t a2 = tc::f2_pack(alpha, alpha);
 #pragma unroll
       for (int i = 0; i < D / 2; ++i) o[i] = tc::fmul2(o[i], a2);
     }
     owed = true;
-    owed_vs = x.vs * exp2_int(-(int)kShift);
+    owed_vs = x.vs * exp2_int(-(int)kTcShift);
     ++page;
   }
 }

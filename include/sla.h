@@ -519,7 +519,7 @@ SLA_API sla_status sla_cache_route(const void* q, const sla_cache_config* cfg, c
  * group's heads and the step's rows give slot s (summed in a fixed order: results do not
  * vary from run to run). Slots at lens[b] and beyond never count, whatever they hold.
  * Scores, maxima, sums and weights are fp32; for the product with V a probability is rounded
- * to fp16, 2^-11 of it, or 2^-40 of the row's largest where that is more.
+ * to fp16, 2^-11 of it, or 2^-33 of the row's largest where that is more.
  * ws: sla_cache_attend_workspace_bytes bytes (with_weight: cache->weight is not NULL),
  * 256-byte aligned, needs no initialisation.
  */

@@ -352,10 +352,11 @@ def test_attend_large_scores_and_one_hot_rows(H):
     out = p.attend(q)
     want, mag, _ = p.o.attend(f64(q), p.lens, [1], None, 0)
     # scores near 2^14 have errors up to 2^14 * 2^-22 = 2^-8 absolute where tokens compete
-    # a weight is held as fp16 of 2^15 times it: its step is 2^-24 / 2^15 at least, so each of
-    # the 333 is off by up to half of that, 2^-40, and one below it counts as 0. Where the one
-    # token that takes all has value 0 in a column, that is all there is
-    floor = 333 * 2.0 ** -40 * np.abs(p.o.rows(0, 0, 333)[1]).max()
+    # a weight is held as fp16 of 2^8 times it at least, the row's largest taken as 1: its step is
+    # 2^-24 / 2^8 at least, so each of the 333 is off by up to half of that, 2^-33, and one below
+    # it counts as 0. Where the one token that takes all has value 0 in a column, that is all
+    # there is
+    floor = 333 * 2.0 ** -33 * np.abs(p.o.rows(0, 0, 333)[1]).max()
     assert np.all(np.abs(f64(out) - want) <= (2.0 ** -8 + 2.0 ** -7) * mag + floor)
 
 
