@@ -37,7 +37,10 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kSlots = 2;       // pages in a warp's ring: keys and values of a tile
 constexpr int kCtasPerSm = 2;
-constexpr int kFewRows = 16;    // more rows of a KV head go to the tcgen05 kernel
+// More rows of a KV head go to the tcgen05 kernel, whose time hardly depends on their number: 8
+// sequences of up to 16001 tokens, 4 KV heads, took this kernel 42, 53, 63 and 88 us at 32, 48,
+// 64 and 96 rows, the other 68 to 70 us; 65536 tokens of one sequence 52 and 59 us at 64.
+constexpr int kFewRows = 64;
 
 // ---------------------------------------------------------------------------
 // instructions
