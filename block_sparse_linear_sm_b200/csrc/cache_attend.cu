@@ -83,6 +83,8 @@ struct Ring {
   unsigned next, end;                       // tiles of the line not yet looked at
   // where tile `next` is: its sequence, KV head, segment, number in it, the segment's tiles
   int b, hk, seg, idx, nb;
+  int2* list;   // shared, a lane's pair: the valid list entries of (sequence, KV head) number list_of
+  int list_of;
   int vrow;  // first row of the values requested next
   // the tile whose pages are requested, and the one after it, whose table entry is being loaded
   Tile req, ahead;
@@ -119,8 +121,19 @@ __device__ __forceinline__ void look_ahead(Ring<D>& r, const CacheView& c, const
   r.has_ahead = false;
   while (r.next < r.end && !r.has_ahead) {
     if (r.idx >= r.nb) locate(r, c, a, l);
-    bool chosen;
-    const int j = tile_block(c, a, r.b, r.hk, r.idx, l.len[r.b], l.fresh[r.b], lane, &chosen);
+    const int first = first_block(a, l.len[r.b], l.fresh[r.b]);
+    bool chosen = a.window == 0;
+    int j = first + r.idx;
+    if (a.sel != nullptr) {
+      if (r.list_of != r.b * c.H_kv + r.hk) {
+        r.list_of = r.b * c.H_kv + r.hk;
+        int2 e;
+        valid_entries(c, a, r.b, r.hk, l.len[r.b], lane, e.x, e.y);
+        r.list[lane] = e;
+      }
+      const int2 e = r.list[lane];
+      j = listed_block(a, r.idx, first, e.x, e.y, &chosen);
+    }
     if (j >= 0) {
       r.ahead.seg = r.seg;
       r.ahead.block = j;
@@ -168,7 +181,7 @@ struct Smem {
   static constexpr int kMerge = kWarps * 8 * NR * kPitch * 4;  // the warps' outputs
   static constexpr int kQ = 8 * NR * D * 2;                    // Q's fragments; the next segment's rows
   static constexpr int off_merge = kRing, off_q = off_merge + kMerge, off_next_q = off_q + kQ, off_misc = off_next_q + kQ;
-  static constexpr int kMisc = 1280;
+  static constexpr int kMisc = 2304;
   static constexpr int off_lines = off_misc + kMisc;
   static size_t bytes(int B) { return off_lines + lines_bytes(B); }
 };
@@ -186,6 +199,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   struct Misc {
     uint64_t bars[kWarps][kSlots];
     float m[kWarps][kRows], l[kWarps][kRows];
+    int2 list[kWarps][32];
     float qs[kRows];  // what a row's scores are multiplied by
     float top[kRows], all[kRows];  // the segment's
     int warp_sums[kWarps];
@@ -239,6 +253,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   fetch_q(sg);
   ring.b = sg.b;
   ring.idx = ring.nb = 0;  // locate it first
+  ring.list = mi.list[warp];
+  ring.list_of = -1;
   // the first tile's keys and values
   look_ahead(ring, c, a, l, lane);
   request_keys(ring, c, a, l, &kmap, lane);
@@ -601,7 +617,7 @@ __device__ void weigh(const CacheView& c, const Step& a, const Lines& l, unsigne
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float z = r + e < a.rows && (a.T == 1 || (r + e) % a.T < n) ? row_lse[r + e] : -INFINITY;
-        if (z != -INFINITY) {
+        if (z > -INFINITY) {  // neither a row that sees nothing nor one that is NaN
           x += tc::ex2_approx(us[e] - z);
           y += tc::ex2_approx(vs[e] - z);
         }

@@ -98,18 +98,13 @@ __device__ __forceinline__ int find_sequence(const Lines& l, int B, unsigned t, 
   return lo;
 }
 
-// Block of tile idx of (b, hk); -1 where it is none. *chosen: the window does not limit it.
-// Called by a whole warp.
-__device__ __forceinline__ int tile_block(const CacheView& c, const Step& a, int b, int hk, int idx, int L, int n,
-                                          int lane, bool* chosen) {
-  const int first = first_block(a, L, n);
-  if (a.sel == nullptr) {
-    *chosen = a.window == 0;
-    return first + idx;
-  }
+// The entries of (b, hk)'s list that count, lane and lane + 32, -1 for the others: those above
+// every earlier one and inside the sequence. Called by a whole warp, which reports the rest.
+__device__ __forceinline__ void valid_entries(const CacheView& c, const Step& a, int b, int hk, int L, int lane, int& e0,
+                                              int& e1) {
   const int32_t* list = a.sel + ((size_t)b * c.H_kv + hk) * a.top_n;
-  const int e0 = lane < a.top_n ? list[lane] : -1, e1 = lane + 32 < a.top_n ? list[lane + 32] : -1;
-  // an entry counts where it is above every earlier one and inside the sequence
+  e0 = lane < a.top_n ? list[lane] : -1;
+  e1 = lane + 32 < a.top_n ? list[lane + 32] : -1;
   int p0 = e0, p1 = e1;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -124,17 +119,32 @@ __device__ __forceinline__ int tile_block(const CacheView& c, const Step& a, int
   if (lane == 0) before0 = before1 = -1;
   before1 = max(before1, all0);
   const int blocks = (L + kBlock - 1) / kBlock;
-  const bool ok0 = e0 >= 0 && e0 > before0 && e0 < blocks, ok1 = e1 >= 0 && e1 > before1 && e1 < blocks;
-  if (idx < a.top_n) {
-    *chosen = true;
-    const int e = __shfl_sync(0xffffffffu, idx < 32 ? e0 : e1, idx & 31);
-    const bool ok = __shfl_sync(0xffffffffu, (int)(idx < 32 ? ok0 : ok1), idx & 31) != 0;
-    if (!ok && e >= 0 && lane == 0) report(c.status, SLA_ERR_DEVICE_CHECK, kDetailCacheSel);
-    return ok ? e : -1;
-  }
-  *chosen = false;
+  const bool bad0 = e0 >= 0 && (e0 <= before0 || e0 >= blocks), bad1 = e1 >= 0 && (e1 <= before1 || e1 >= blocks);
+  if (bad0 || bad1) report(c.status, SLA_ERR_DEVICE_CHECK, kDetailCacheSel);
+  if (bad0 || e0 < 0) e0 = -1;
+  if (bad1 || e1 < 0) e1 = -1;
+}
+
+// Block of tile idx of a sequence whose list's valid entries the warp holds; -1 where it is
+// none. *chosen: the window does not limit it.
+__device__ __forceinline__ int listed_block(const Step& a, int idx, int first, int e0, int e1, bool* chosen) {
+  *chosen = idx < a.top_n;
+  if (idx < a.top_n) return __shfl_sync(0xffffffffu, idx < 32 ? e0 : e1, idx & 31);
   const int j = first + idx - a.top_n;
-  return __any_sync(0xffffffffu, (ok0 && e0 == j) || (ok1 && e1 == j)) ? -1 : j;
+  return __any_sync(0xffffffffu, e0 == j || e1 == j) ? -1 : j;
+}
+
+// The same for a tile by itself.
+__device__ __forceinline__ int tile_block(const CacheView& c, const Step& a, int b, int hk, int idx, int L, int n,
+                                          int lane, bool* chosen) {
+  const int first = first_block(a, L, n);
+  if (a.sel == nullptr) {
+    *chosen = a.window == 0;
+    return first + idx;
+  }
+  int e0, e1;
+  valid_entries(c, a, b, hk, L, lane, e0, e1);
+  return listed_block(a, idx, first, e0, e1, chosen);
 }
 
 // A segment of the line: one row group of one KV head of one sequence, with its tiles.

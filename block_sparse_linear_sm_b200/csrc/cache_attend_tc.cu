@@ -358,7 +358,8 @@ __device__ bool rows_of_step(const CacheView& c, const Step& a, const Lines& l, 
   size_t qrow = 0;
   bool owed = false;  // P V of page - 1
 
-  auto collect = [&](unsigned i) -> bool {  // O += v_scale * (P V)
+  // O += v_scale * (P V) of page i, with `meanwhile` done while the first columns are on their way
+  auto collect = [&](unsigned i, auto meanwhile) -> bool {
     const unsigned k = i & 1;
     if (!wait_all(&mi.o_full[k], i >> 1, mi)) return false;
     tc::fence_after_sync();
@@ -368,6 +369,7 @@ __device__ bool rows_of_step(const CacheView& c, const Step& a, const Lines& l, 
       uint32_t x[32], y[32];
       tc::tmem_ld32(lanes + Cols<D>::acc + k * D + 64 * u, x);
       tc::tmem_ld32(lanes + Cols<D>::acc + k * D + 64 * u + 32, y);
+      if (u == 0) meanwhile();
       tc::tmem_ld_wait();
 #pragma unroll
       for (int i2 = 0; i2 < 16; ++i2) {
@@ -385,7 +387,7 @@ __device__ bool rows_of_step(const CacheView& c, const Step& a, const Lines& l, 
     Info x;
     if (!read_info(mi, e, lane, &x)) return false;
     if (x.seg != seg) {
-      if (owed && !collect(page - 1)) return false;
+      if (owed && !collect(page - 1, [] {})) return false;
       owed = false;
       if (seg >= 0) {
         const int sr = seg % (int)per, nb = l.cum[b + 1] - l.cum[b];
@@ -527,10 +529,13 @@ __device__ bool rows_of_step(const CacheView& c, const Step& a, const Lines& l, 
     sum += tc::f2_lo(s2[0]) + tc::f2_hi(s2[0]);
     // this buffer's P was read by the product that was collected a page ago
     tc::tmem_st32(lanes + Cols<D>::p + 32 * k, pk);
-    tc::tmem_st_wait();
-    tc::fence_before_sync();
-    arrive_warp(&mi.p_full[k], lane);
-    if (owed && !collect(page - 1)) return false;
+    auto hand_over = [&] {
+      tc::tmem_st_wait();
+      tc::fence_before_sync();
+      arrive_warp(&mi.p_full[k], lane);
+    };
+    if (!owed) hand_over();
+    else if (!collect(page - 1, hand_over)) return false;
     if (any_raise) {
       const uint64_t a2 = tc::f2_pack(alpha, alpha);
 #pragma unroll

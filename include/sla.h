@@ -478,8 +478,8 @@ SLA_API sla_status sla_cache_validate_config(const sla_cache_config* cfg);
  * but for results below 2^-126). weight becomes 0 in the new slots.
  * Elements that are NaN are stored as 0 and magnitudes above 2^120 as 2^120, with the
  * status word set. A sequence whose length or n_new is out of range, or that would outgrow
- * the table, is left alone with the status word set, lens_out[b] = lens[b]; a block whose
- * page number is out of range likewise.
+ * the table, is left alone with the status word set, lens_out[b] = lens[b]. A block whose
+ * page number is out of range is left out, also with the status word set.
  */
 SLA_API sla_status sla_cache_append(const void* k, const void* v, const sla_cache_config* cfg,
                                     const sla_cache* cache, int32_t T, const int32_t* lens,
@@ -495,7 +495,8 @@ SLA_API sla_status sla_cache_append(const void* k, const void* v, const sla_cach
  *   lens   int32 [B]: cached tokens, the step's own included (as after sla_cache_append)
  *   n_new  int32 [B] or NULL (T): valid query rows, the last n_new[b] cached tokens
  *   sel    int32 [B, H_kv, top_n], 1 <= top_n <= 64: ascending, -1 behind the last
- * A past block whose page number is out of range scores -inf and is never picked.
+ * A past block whose page number is out of range scores -inf and is never picked; where a
+ * query or mean holds a NaN nothing is.
  */
 SLA_API sla_status sla_cache_route(const void* q, const sla_cache_config* cfg, const sla_cache* cache,
                                    int32_t T, const int32_t* lens, const int32_t* n_new,
@@ -517,7 +518,9 @@ SLA_API sla_status sla_cache_route(const void* q, const sla_cache_config* cfg, c
  * over, and one that is too large or not above those before it is left out with the status
  * word set. With cache->weight, weight[b, hk, s] grows by the probabilities that the
  * group's heads and the step's rows give slot s (summed in a fixed order: results do not
- * vary from run to run). Slots at lens[b] and beyond never count, whatever they hold.
+ * vary from run to run). Slots at lens[b] and beyond never count, whatever they hold. A
+ * query row that holds a NaN or an infinity becomes NaN and adds no weight; other rows do
+ * not notice.
  * Scores, maxima, sums and weights are fp32; for the product with V a probability is rounded
  * to fp16, 2^-11 of it, or 2^-33 of the row's largest where that is more.
  * ws: sla_cache_attend_workspace_bytes bytes (with_weight: cache->weight is not NULL),

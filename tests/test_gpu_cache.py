@@ -405,6 +405,22 @@ def test_attend_nan_query_stays_in_its_row(H):
     assert torch.isnan(out[0, 3, 1]).all() and torch.isnan(out[1, 6, 0]).all()
 
 
+def test_attend_nan_query_adds_no_weight():
+    p = Pair(B=2, H=4, H_kv=2, d=64, seed=19)
+    p.fill([100, 70])
+    p.c.weight.zero_()
+    q = p.queries(2)
+    p.attend(q)
+    want = p.c.weight.clone()
+    q[0, 1, 0, 3] = float("nan")
+    p.c.weight.zero_()
+    p.attend(q)
+    assert torch.isfinite(p.c.weight).all()
+    assert torch.equal(p.c.weight[0, 1], want[0, 1]) and torch.equal(p.c.weight[1], want[1])
+    # three of the four rows of the KV head are left
+    assert abs(p.c.weight[0, 0].sum().item() - 3) < 3e-5 and abs(want[0, 0].sum().item() - 4) < 4e-5
+
+
 def test_attend_shared_pages():
     """Sequences may share pages that are only read."""
     p = Pair(B=3, H=4, H_kv=2, d=64, max_blocks=4, seed=15)
@@ -433,6 +449,31 @@ def test_attend_many_rows():
     p = Pair(B=1, H=16, H_kv=1, d=128, max_blocks=4, seed=17)
     p.fill([190])
     p.check_attend(p.queries(64))
+
+
+LONGEST = 4096 * 64
+
+
+@pytest.mark.parametrize("T,H", [(1, 2), (1, 16), (2, 70)])
+def test_attend_longest_sequence(T, H):
+    """4096 blocks, the last one open, beside a sequence of one token; the long one's pages repeat."""
+    p = Pair(B=2, H=H, H_kv=2 if H == 2 else 1, d=64, max_blocks=4096, kind=INT8, seed=20, garbage=False)
+    p.c.k.view(torch.uint8).zero_(), p.c.v.view(torch.uint8).zero_()
+    few = np.arange(7)
+    p.table[0], p.table[1, 0] = few[np.arange(4096) % 7], 7
+    p.o.table = p.table
+    p.c.block_table.copy_(i32(p.table))
+    rng = np.random.default_rng(1)
+    for name in ("k", "v"):
+        codes = rng.integers(-60, 61, getattr(p.o, name)[:8].shape)
+        getattr(p.o, name)[:8] = codes
+        getattr(p.c, name)[:8] = torch.from_numpy(codes.astype(np.int8)).cuda()
+    for name, dev in (("ks", p.c.k_scale), ("vs", p.c.v_scale)):
+        getattr(p.o, name)[:] = 2.0 ** -5
+        dev.fill_(2.0 ** -5)
+    p.c.weight.zero_()
+    p.lens = np.array([LONGEST - 5, 1])
+    p.check_attend(p.queries(T), n_new=[T, min(T, 1)])
 
 
 @pytest.mark.parametrize("T", [2, 9])
@@ -584,6 +625,53 @@ def test_evict_long():
     p.check(dst)
 
 
+def test_evict_longest():
+    """262144 slots: every weight of a CTA's run in shared memory."""
+    p = Pair(B=1, H=1, H_kv=1, d=64, max_blocks=4096, spare=8, seed=36, garbage=False)
+    p.lens = np.array([4096 * 64])
+    p.o.ks[:], p.o.vs[:] = 1.0, 1.0
+    p.c.k_scale.fill_(1.0), p.c.v_scale.fill_(1.0)
+    codes = np.random.default_rng(6).integers(0, 120, p.o.k.shape)      # e4m3 bytes of positive numbers
+    p.o.k, p.o.v = co.code_table(E4M3)[codes], co.code_table(E4M3)[codes[::-1]]
+    p.c.k.view(torch.uint8).copy_(torch.from_numpy(codes.astype(np.uint8)))
+    p.c.v.view(torch.uint8).copy_(torch.from_numpy(codes[::-1].astype(np.uint8)))
+    p.o.weight[:] = np.random.default_rng(7).integers(0, 5000, p.o.weight.shape) / 64.0
+    p.c.weight.copy_(torch.from_numpy(p.o.weight))
+    dst, _ = run_evict(p, 500, 4, 100, False)
+    p.check(dst)
+
+
+def test_evict_in_a_captured_graph():
+    """Replayed twice on the same cache, other weights each time, in place and packed again."""
+    p = Pair(B=2, H=2, H_kv=2, d=64, max_blocks=10, kind=INT8, spare=0, seed=37)
+    p.fill([600, 333])
+    budget, nd = 200, 4
+    lens, lens_out = i32(p.lens), torch.zeros(2, dtype=torch.int32, device="cuda")
+    dst = i32(p.table[:, :nd])
+    kept = torch.zeros(2, 2, budget, dtype=torch.int32, device="cuda")
+    ws = torch.empty(sla.sla_cache_evict_workspace_bytes(p.cfg, budget), dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        sla.sla_cache_evict(p.cfg, p.c, lens, budget, 4, 50, dst, p.c.weight, kept, lens_out, ws)
+    for step in range(2):
+        w = np.random.default_rng(step).random(p.o.weight.shape).astype(np.float32)
+        p.o.weight[:] = w
+        p.c.weight.copy_(torch.from_numpy(w))
+        lens.copy_(i32(p.lens))
+        g.replay()
+        out = p.o.weight.copy()
+        want = p.o.evict(p.lens, budget, 4, 50, p.table[:, :nd], out)
+        np.testing.assert_array_equal(kept.cpu().numpy(), want)
+        p.o.weight = out
+        p.lens = np.minimum(p.lens, budget)
+        p.check()
+        p.append(*p.kv(130))
+        p.check()
+    p.status()
+
+
 def test_evict_reports_bad_pages_and_lengths():
     p = Pair(B=3, H=1, H_kv=1, d=64, max_blocks=4, spare=6, seed=34)
     p.fill([200, 200, 200])
@@ -699,6 +787,29 @@ def test_streams_and_captured_steps():
             assert np.all(np.abs(f64(out) - want) <= 2.0 ** -8 * np.abs(want) + (2.0 ** -11 + 2.0 ** -16) * mag)
     assert lens.tolist() == p.lens.tolist()
     p.status()
+
+
+def test_calls_on_a_given_stream():
+    """stream= instead of the current one: ordered with work on that stream only."""
+    p = Pair(B=2, H=4, H_kv=2, d=64, max_blocks=4, seed=61)
+    p.fill([130, 40])
+    s = torch.cuda.Stream()
+    k, v = p.kv(3)
+    q = p.queries(3)
+    lens, out, sel = i32(p.lens), torch.empty_like(q), torch.zeros(2, 2, 2, dtype=torch.int32, device="cuda")
+    ws = torch.empty(sla.sla_cache_attend_workspace_bytes(p.cfg, 3, 2, 9, True), dtype=torch.uint8, device="cuda")
+    new = torch.empty_like(lens)
+    torch.cuda.synchronize()
+    sla.sla_cache_append(k, v, p.cfg, p.c, lens, None, new, stream=s)
+    sla.sla_cache_route(q, p.cfg, p.c, new, None, sel, stream=s.cuda_stream)
+    sla.sla_cache_attend(q, p.cfg, p.c, new, None, sel, 9, out, ws, stream=s)
+    assert sla.sla_check_device_status(p.c.status, stream=s) == (0, 0)
+    p.lens = p.o.append(f64(k), f64(v), p.lens, [3, 3])
+    want_sel, gap = p.o.route(f64(q), p.lens, [3, 3], 2)
+    assert gap > 1e-9
+    np.testing.assert_array_equal(sel.cpu().numpy(), want_sel)
+    want, mag, _ = p.o.attend(f64(q), p.lens, [3, 3], want_sel, 9)
+    assert np.all(np.abs(f64(out) - want) <= 2.0 ** -8 * np.abs(want) + (2.0 ** -11 + 2.0 ** -16) * mag)
 
 
 def test_calls_on_two_streams_at_once():
