@@ -300,7 +300,8 @@ __host__ __device__ inline int select_run(int n, int threads) {
 template <int kSelThreads>
 __global__ void __cluster_dims__(kSelCluster, 1, 1) __launch_bounds__(kSelThreads)
     evict_select_kernel(const CacheView c, const int32_t* __restrict__ lens, int budget, int n_sink, int n_recent,
-                        int32_t* __restrict__ kept, int32_t* lens_out, int* __restrict__ flags, int n_flags) {
+                        int32_t* __restrict__ kept, int32_t* lens_out, const int32_t* __restrict__ dst_table,
+                        int same_weights, int* __restrict__ flags, int n_flags, int* __restrict__ rows) {
   extern __shared__ uint32_t keys[];  // [select_run(cap)]
   __shared__ int hist[2][256], total[256];
   __shared__ int s_digit, s_rest;
@@ -316,11 +317,31 @@ __global__ void __cluster_dims__(kSelCluster, 1, 1) __launch_bounds__(kSelThread
     lens_out[b] = m;
   }
   // what the move's CTAs of this sequence and head count and signal with
-  for (int i = rank * kSelThreads + tid; i < n_flags; i += kSelCluster * kSelThreads) flags[(size_t)bh * n_flags + i] = 0;
+  int* flag = flags + (size_t)bh * n_flags;
+  for (int i = rank * kSelThreads + tid; i < n_flags - 1; i += kSelCluster * kSelThreads) flag[i] = 0;
   int32_t* out = kept + (size_t)bh * budget;
+  rows += (size_t)bh * budget;
+  // kept slot i comes from row `slot` of the sequence; rows: where that is in the pool, -1 nowhere
+  auto page_of = [&](int slot) { return slot < n ? c.table[(size_t)b * c.max_blocks + slot / kBlock] : 0; };
+  auto keep = [&](int i, int slot, int page) {
+    out[i] = slot;
+    const bool there = page >= 0 && page < c.n_pages;
+    if (!there) report(c.status, SLA_ERR_DEVICE_CHECK, kDetailCachePage);
+    rows[i] = there ? (page * c.H_kv + hk) * kBlock + slot % kBlock : -1;
+  };
   for (int i = m + rank * kSelThreads + tid; i < budget; i += kSelCluster * kSelThreads) out[i] = -1;
+  // whether the move has to: it packs some block in place, or its weights (one warp)
+  auto tell = [&] {
+    bool any = same_weights != 0;
+    for (int i = lane; i * kBlock < m; i += 32)
+      any |= dst_table[(size_t)b * (n_flags - 2) + i] == c.table[(size_t)b * c.max_blocks + i];
+    any = __any_sync(0xffffffffu, any);
+    if (lane == 0) flag[n_flags - 1] = any;
+  };
+  const bool teller = rank == kSelCluster - 1 && warp == kSelThreads / 32 - 1;
   if (n <= budget) {  // the same for the whole cluster
-    for (int i = rank * kSelThreads + tid; i < n; i += kSelCluster * kSelThreads) out[i] = i;
+    if (teller) tell();
+    for (int i = rank * kSelThreads + tid; i < n; i += kSelCluster * kSelThreads) keep(i, i, page_of(i));
     return;
   }
   const float* w = c.weight + (size_t)bh * c.cap;
@@ -422,14 +443,18 @@ __global__ void __cluster_dims__(kSelCluster, 1, 1) __launch_bounds__(kSelThread
     eq += equal[i];
   }
   at += min(eq, rest);
+  if (teller) tell();
+  int next_page = page_of(wa + lane);
   for (int i = wa + lane; i - lane < wz; i += 32) {
+    const int page = next_page;
+    next_page = page_of(i + 32);
     const bool held = i < wz && (i < lo || i >= hi), in = i < wz && !held && want > 0;
     const uint32_t key = in ? keys[i - a] : 0u;
     const uint32_t below = (1u << lane) - 1u;
     const uint32_t eqs = __ballot_sync(0xffffffffu, in && key == prefix);
     const bool take = held || (in && (key > prefix || (key == prefix && eq + __popc(eqs & below) < rest)));
     const uint32_t takes = __ballot_sync(0xffffffffu, take);
-    if (take) out[at + __popc(takes & below)] = i;
+    if (take) keep(at + __popc(takes & below), i, page);
     at += __popc(takes);
     eq += __popc(eqs);
   }
@@ -443,9 +468,9 @@ __global__ void __cluster_dims__(kSelCluster, 1, 1) __launch_bounds__(kSelThread
 // place it still holds rows that other new blocks load: those that keep slots of old block
 // j are one or two (kept is ascending and kept[i] >= i), all of them at or before j. So every
 // CTA signals when its loads are done, and one that writes in place first waits for those
-// few. CTAs take their block from a counter of their sequence and head when they start: one
-// that waits has only such before it that have started, and none of them waits before it has
-// signalled.
+// few. CTAs of a sequence that is packed in place take their block from a counter when they
+// start: one that waits has only such before it that have started, and none of them waits
+// before it has signalled.
 // ---------------------------------------------------------------------------
 // first i in [0, m) with from[i] >= slot, m if none
 __device__ __forceinline__ int first_kept(const int32_t* from, int m, int slot) {
@@ -459,56 +484,57 @@ __device__ __forceinline__ int first_kept(const int32_t* from, int m, int slot) 
 }
 
 template <int KIND, int D>
-__global__ void __launch_bounds__(kCta) evict_move_kernel(const CacheView c, const int32_t* kept,
+__global__ void __launch_bounds__(kCta, 5) evict_move_kernel(const CacheView c, const int32_t* kept,
                                                           const int32_t* lens, int budget, const int32_t* dst_table,
-                                                          float* weight_out, int* flags, int n_flags) {
+                                                          float* weight_out, int* flags, int n_flags, const int* rows) {
   constexpr int C = D / 16;
   constexpr int NT = kBlock * C / kCta;
   __shared__ uint32_t slots[2][kCta / 32];
   __shared__ __align__(16) uint8_t tile[kBlock * D];
   __shared__ float4 parts[kCta];
-  __shared__ int s_slot[kBlock], s_ph[kBlock];
+  __shared__ int s_row[kBlock];
   __shared__ int s_j, s_late;
   const int tid = threadIdx.x, nd = (budget + kBlock - 1) / kBlock;
   const int bh = blockIdx.x / nd, b = bh / c.H_kv, hk = bh % c.H_kv;
   bool bad = false;
   const int m = min(checked_len(lens, b, c.cap, &bad), budget);
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  int* done = flags + (size_t)bh * n_flags;  // [nd] signals, then the counter
-  if (tid == 0) {
-    s_j = atomicAdd(&done[nd], 1);
-    s_late = 0;
-  }
-  __syncthreads();
-  const int j = s_j, first = j * kBlock;
-  if (first >= m) return;
+  int* done = flags + (size_t)bh * n_flags;  // [nd] signals, a counter, whether they are needed
   const int32_t* from = kept + (size_t)bh * budget;
-  if (tid < kBlock) {
-    const int slot = first + tid < m ? from[first + tid] : -1;
-    const int page = slot < 0 ? -1 : checked_page(c, b, slot / kBlock);
-    s_slot[tid] = slot;
-    s_ph[tid] = page < 0 ? -1 : page * c.H_kv + hk;
+  rows += (size_t)bh * budget;
+  // the block that the launch order gives is on its way before it is known whether it may be taken
+  int j = blockIdx.x - bh * nd;
+  const bool ordered = done[nd + 1] != 0;
+  if (tid < kBlock) s_row[tid] = j * kBlock + tid < m ? rows[j * kBlock + tid] : -1;
+  int to_page = dst_table[(size_t)b * nd + j];
+  if (tid == 0) s_late = 0;
+  if (ordered) {
+    if (tid == 0) s_j = atomicAdd(&done[nd], 1);
+    __syncthreads();
+    j = s_j;
+    if (tid < kBlock) s_row[tid] = j * kBlock + tid < m ? rows[j * kBlock + tid] : -1;
+    to_page = dst_table[(size_t)b * nd + j];
   }
-  const int to_page = dst_table[(size_t)b * nd + j];
-  const bool in_place = to_page == c.table[(size_t)b * c.max_blocks + j];
+  const int first = j * kBlock;
+  if (first >= m) return;
   __syncthreads();
   uint4 kc[NT], vc[NT];
   float ks[NT], vs[NT];
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
-    const int task = tid + kCta * i, r = task / C, ch = task % C, ph = s_ph[r];
+    const int task = tid + kCta * i, r = task / C, ch = task % C, row = s_row[r];
     kc[i] = vc[i] = make_uint4(0u, 0u, 0u, 0u);
     ks[i] = vs[i] = 0.f;
-    if (ph >= 0) {
-      const size_t at = ((size_t)ph * kBlock + s_slot[r] % kBlock) * D + ch * 16;
+    if (row >= 0) {
+      const size_t at = (size_t)row * D + ch * 16;
       kc[i] = *reinterpret_cast<const uint4*>(c.k + at);
       vc[i] = *reinterpret_cast<const uint4*>(c.v + at);
-      ks[i] = c.k_scale[ph];
-      vs[i] = c.v_scale[ph];
+      ks[i] = c.k_scale[row / kBlock];
+      vs[i] = c.v_scale[row / kBlock];
     }
   }
   const size_t wrow = (size_t)bh * c.cap;
-  const float w = tid < kBlock && s_slot[tid] >= 0 ? c.weight[wrow + s_slot[tid]] : 0.f;
+  const float w = tid < kBlock && first + tid < m ? c.weight[wrow + from[first + tid]] : 0.f;
   float ka = 0.f, va = 0.f;
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
@@ -529,8 +555,8 @@ __global__ void __launch_bounds__(kCta) evict_move_kernel(const CacheView c, con
     vm = max(vm, slots[1][i]);
   }
   if (tid == 0) {
-    asm volatile("fence.acq_rel.gpu;\n\tst.relaxed.gpu.global.s32 [%0], 1;" ::"l"(done + j) : "memory");
-    if (in_place || weight_out == c.weight) {
+    if (ordered) asm volatile("fence.acq_rel.gpu;\n\tst.relaxed.gpu.global.s32 [%0], 1;" ::"l"(done + j) : "memory");
+    if (weight_out == c.weight || to_page == c.table[(size_t)b * c.max_blocks + j]) {
       const int i0 = first_kept(from, m, first), i1 = first_kept(from, m, first + kBlock);
       const uint64_t t0 = tc::globaltimer();
       for (int y = i0 / kBlock; y * kBlock < i1 && y < j; ++y) {
@@ -612,12 +638,12 @@ sla_status sla_cache_append(const void* k, const void* v, const sla_cache_config
   return cudaGetLastError() == cudaSuccess ? SLA_OK : SLA_ERR_CUDA;
 }
 
-// ints a (sequence, KV head): a signal of each new block, a counter
-static int evict_flags(int budget) { return (budget + kBlock - 1) / kBlock + 1; }
+// ints a (sequence, KV head): a signal of each new block, a counter, whether they are needed
+static int evict_flags(int budget) { return (budget + kBlock - 1) / kBlock + 2; }
 
 size_t sla_cache_evict_workspace_bytes(const sla_cache_config* cfg, int32_t budget) {
   if (check_sizes(cfg) != SLA_OK || budget < 1 || budget > cfg->max_blocks * kBlock) return 0;
-  return align_up((size_t)cfg->B * cfg->H_kv * evict_flags(budget) * sizeof(int), 256);
+  return align_up((size_t)cfg->B * cfg->H_kv * ((size_t)evict_flags(budget) + budget) * sizeof(int), 256);
 }
 
 sla_status sla_cache_evict(const sla_cache_config* cfg, const sla_cache* cache, const int32_t* lens, int32_t budget,
@@ -633,12 +659,13 @@ sla_status sla_cache_evict(const sla_cache_config* cfg, const sla_cache* cache, 
     return SLA_ERR_INVALID_ARG;
   if (budget < 1 || budget > c.cap || n_sink < 0 || n_recent < 0 || n_sink > budget - n_recent)
     return SLA_ERR_INVALID_ARG;
-  if ((int64_t)c.B * c.H_kv * (evict_flags(budget) - 1) >= ((int64_t)1 << 31)) return SLA_ERR_UNSUPPORTED;  // grid
+  if ((int64_t)c.B * c.H_kv * (evict_flags(budget) - 2) >= ((int64_t)1 << 31)) return SLA_ERR_UNSUPPORTED;  // grid
   if (!ws || !aligned_to(ws, 256) || ws_bytes < sla_cache_evict_workspace_bytes(cfg, budget))
     return SLA_ERR_WORKSPACE;
   cudaStream_t s = (cudaStream_t)stream;
   int* flags = (int*)ws;
-  const int n_flags = evict_flags(budget), nd = n_flags - 1;
+  const int n_flags = evict_flags(budget), nd = n_flags - 2;
+  int* rows = flags + (size_t)c.B * c.H_kv * n_flags;
   // The keys take turns of one a thread: 1024 threads where all CTAs are resident at once with
   // them (65536 slots of 4 heads: 31 us for the call, 35 with 512), else 512 (64 heads of 16384
   // slots: 60 us, 72 with 1024, whose 512 CTAs came in two waves).
@@ -647,7 +674,7 @@ sla_status sla_cache_evict(const sla_cache_config* cfg, const sla_cache* cache, 
                              select_run(kMaxBlocks * kBlock, threads) * (int)sizeof(uint32_t)) != cudaSuccess)
       return;
     kernel<<<c.B * c.H_kv * kSelCluster, threads, select_run(c.cap, threads) * (int)sizeof(uint32_t), s>>>(
-        c, lens, budget, n_sink, n_recent, kept, lens_out, flags, n_flags);
+        c, lens, budget, n_sink, n_recent, kept, lens_out, dst_table, weight_out == c.weight, flags, n_flags, rows);
   };
   if (c.B * c.H_kv * kSelCluster <= 2 * 148) select(evict_select_kernel<1024>, 1024);
   else select(evict_select_kernel<512>, 512);
@@ -663,7 +690,7 @@ sla_status sla_cache_evict(const sla_cache_config* cfg, const sla_cache* cache, 
   launch.numAttrs = 1;
   auto run = [&](auto kernel) {
     return cudaLaunchKernelEx(&launch, kernel, c, (const int32_t*)kept, lens, (int)budget, dst_table, weight_out, flags,
-                              n_flags);
+                              n_flags, (const int*)rows);
   };
   cudaError_t e;
   if (c.kind == SLA_CACHE_E4M3)
