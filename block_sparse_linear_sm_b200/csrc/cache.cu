@@ -152,7 +152,11 @@ __device__ __forceinline__ void write_mean(const uint8_t* tile, float scale, flo
 // ---------------------------------------------------------------------------
 // append: one CTA a (block that may be written, KV head, sequence), keys and values apart.
 // A thread holds its 16-element chunks as the bf16 words that it loaded (8 registers) and
-// takes the largest magnitude on their bits, which order like the magnitudes.
+// takes the largest magnitude on their bits, which order like the magnitudes. One pass: a page
+// is read, its scale found with one barrier, and written. Bound by HBM for prompts (2 x 12 x
+// 32760 rows of 128, int8: 79 us on the device, 6.0 TB/s of the 476 MB it cannot do without),
+// by its chain of loads (length, page, rows, barrier) for a step's one token (64 sequences x 8
+// heads: 5.4 us).
 // ---------------------------------------------------------------------------
 template <int KIND, int D>
 __global__ void __launch_bounds__(kCta) append_kernel(const CacheView c, const __nv_bfloat16* __restrict__ k_new,
@@ -266,7 +270,9 @@ __global__ void __launch_bounds__(kCta) append_kernel(const CacheView c, const _
 // time: the CTAs' histograms are added through distributed shared memory. Weights crowd in
 // few values of the first digit, so there lanes with the same one count together. Then
 // every CTA counts its run, takes its place from the counts of those before, and writes its
-// kept slots in order.
+// kept slots in order, with the pool rows that they are in. Bound by its chain of steps (four
+// digits of a pass, a cluster barrier and a scan each), not by the 4 bytes a slot: 65536 slots
+// of 4 heads 19 us, up to 16384 of 64 heads 21 us.
 // ---------------------------------------------------------------------------
 constexpr int kSelCluster = 8;
 
@@ -470,7 +476,8 @@ __global__ void __cluster_dims__(kSelCluster, 1, 1) __launch_bounds__(kSelThread
 // CTA signals when its loads are done, and one that writes in place first waits for those
 // few. CTAs of a sequence that is packed in place take their block from a counter when they
 // start: one that waits has only such before it that have started, and none of them waits
-// before it has signalled.
+// before it has signalled. Bound by the latency of the gather (place, rows, barrier, write)
+// with 40 KB or so in flight an SM: 8 x 8 heads x 4001 rows 35 us (131 MB, 3.8 TB/s).
 // ---------------------------------------------------------------------------
 // first i in [0, m) with from[i] >= slot, m if none
 __device__ __forceinline__ int first_kept(const int32_t* from, int m, int slot) {

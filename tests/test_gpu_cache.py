@@ -685,6 +685,17 @@ def test_evict_reports_bad_pages_and_lengths():
     sla.sla_cache_evict(p.cfg, p.c, i32(p.lens), 100, 0, 0, i32(dst), w, kept, lens_out, ws)
     p.status((sla.SLA_ERR_DEVICE_CHECK, 110))
     assert torch.equal(p.c.k.view(torch.uint8), before)
+    # a source page out of range: its tokens become 0, the others move
+    good = p.spare.reshape(3, 2)
+    p.c.block_table[1, 0] = p.cfg.n_pages
+    sla.sla_cache_evict(p.cfg, p.c, i32(p.lens), 100, 0, 100, i32(good), w, kept, lens_out, ws)
+    p.status()                                   # the kept tokens are in blocks 1 to 3
+    sla.sla_cache_evict(p.cfg, p.c, i32(p.lens), 100, 100, 0, i32(good), w, kept, lens_out, ws)
+    p.status((sla.SLA_ERR_DEVICE_CHECK, 110))
+    moved = codes_of(p.c.k)[good]
+    assert not moved[1, 0].any() and moved[1, 1, :, :36].any() and moved[0, 0].any() and moved[2, 0].any()
+    p.c.block_table.copy_(i32(p.table))
+    before = p.c.k.view(torch.uint8).clone()
     sla.sla_cache_evict(p.cfg, p.c, i32([-1, 257, 0]), 100, 0, 0, i32(dst), w, kept, lens_out, ws)
     p.status((sla.SLA_ERR_DEVICE_CHECK, 111))
     assert lens_out.tolist() == [0, 0, 0] and (kept == -1).all()
