@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 
   // this CTA's run of the line
   const unsigned per = c.H_kv * a.groups, total = (unsigned)l.cum[c.B] * per;
-  const unsigned run = max((total + gridDim.x - 1) / gridDim.x, a.min_run);
+  const unsigned run = a.min_run * ((total + gridDim.x * a.min_run - 1) / (gridDim.x * a.min_run));
   const unsigned lo = min(total, blockIdx.x * run), hi = min(total, lo + run);
   if (lo >= hi) return;
 
@@ -668,7 +668,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const CacheView c, c
   Lines l;
   scan_lines(c, a, smem, &l, warp_sums);
   const unsigned per = c.H_kv * a.groups, total = (unsigned)l.cum[c.B] * per;
-  const unsigned run = max((total + ctas - 1) / ctas, a.min_run);
+  const unsigned run = a.min_run * ((total + ctas * a.min_run - 1) / (ctas * a.min_run));
   if (blockIdx.x >= segs) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     weigh(c, a, l, ((blockIdx.x - segs) * gridDim.y + blockIdx.y) * W + warp, (gridDim.x - segs) * gridDim.y * W, lane,
