@@ -171,6 +171,8 @@ __global__ void __launch_bounds__(kCta) append_kernel(const CacheView c, const _
   __shared__ float4 parts[kCta];
   const int hk = blockIdx.x % c.H_kv, jj = blockIdx.x / c.H_kv, b = blockIdx.y;
   const bool is_k = blockIdx.z == 0;
+  wait_for_previous();
+  let_next_start();
   const int L = lens[b], n = n_new ? n_new[b] : T;
   const bool bad = L < 0 || L > c.cap || n < 0 || n > T || L + n > c.cap;
   if (blockIdx.x == 0 && is_k && threadIdx.x == 0) {
@@ -315,7 +317,8 @@ __global__ void __cluster_dims__(kSelCluster, 1, 1) __launch_bounds__(kSelThread
   const int bh = blockIdx.x / kSelCluster, b = bh / c.H_kv, hk = bh % c.H_kv;
   const int rank = (int)cluster_rank();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  asm volatile("griddepcontrol.launch_dependents;");
+  wait_for_previous();
+  let_next_start();
   bool bad = false;
   const int n = checked_len(lens, b, c.cap, &bad), m = min(n, budget);
   if (hk == 0 && rank == 0 && tid == 0) {
@@ -503,9 +506,10 @@ __global__ void __launch_bounds__(kCta, 5) evict_move_kernel(const CacheView c, 
   __shared__ int s_j, s_late;
   const int tid = threadIdx.x, nd = (budget + kBlock - 1) / kBlock;
   const int bh = blockIdx.x / nd, b = bh / c.H_kv, hk = bh % c.H_kv;
+  wait_for_previous();
+  let_next_start();
   bool bad = false;
   const int m = min(checked_len(lens, b, c.cap, &bad), budget);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   int* done = flags + (size_t)bh * n_flags;  // [nd] signals, a counter, whether they are needed
   const int32_t* from = kept + (size_t)bh * budget;
   rows += (size_t)bh * budget;
@@ -633,16 +637,13 @@ sla_status sla_cache_append(const void* k, const void* v, const sla_cache_config
   const dim3 grid((unsigned)(touched * c.H_kv), (unsigned)c.B, 2);
   cudaStream_t s = (cudaStream_t)stream;
   auto run = [&](auto kernel) {
-    kernel<<<grid, 256, 0, s>>>(c, (const __nv_bfloat16*)k, (const __nv_bfloat16*)v, T, lens, n_new, lens_out);
+    return launch_overlapped(kernel, grid, kCta, 0, s, c, (const __nv_bfloat16*)k, (const __nv_bfloat16*)v, (int)T, lens,
+                             n_new, lens_out);
   };
-  if (c.kind == SLA_CACHE_E4M3) {
-    if (c.d == 128) run(append_kernel<SLA_CACHE_E4M3, 128>);
-    else run(append_kernel<SLA_CACHE_E4M3, 64>);
-  } else {
-    if (c.d == 128) run(append_kernel<SLA_CACHE_INT8, 128>);
-    else run(append_kernel<SLA_CACHE_INT8, 64>);
-  }
-  return cudaGetLastError() == cudaSuccess ? SLA_OK : SLA_ERR_CUDA;
+  cudaError_t e;
+  if (c.kind == SLA_CACHE_E4M3) e = c.d == 128 ? run(append_kernel<SLA_CACHE_E4M3, 128>) : run(append_kernel<SLA_CACHE_E4M3, 64>);
+  else e = c.d == 128 ? run(append_kernel<SLA_CACHE_INT8, 128>) : run(append_kernel<SLA_CACHE_INT8, 64>);
+  return e == cudaSuccess ? SLA_OK : SLA_ERR_CUDA;
 }
 
 // ints a (sequence, KV head): a signal of each new block, a counter, whether they are needed
@@ -677,29 +678,20 @@ sla_status sla_cache_evict(const sla_cache_config* cfg, const sla_cache* cache, 
   // them (65536 slots of 4 heads: 31 us for the call, 35 with 512), else 512 (64 heads of 16384
   // slots: 60 us, 72 with 1024, whose 512 CTAs came in two waves).
   auto select = [&](auto kernel, int threads) {
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             select_run(kMaxBlocks * kBlock, threads) * (int)sizeof(uint32_t)) != cudaSuccess)
-      return;
-    kernel<<<c.B * c.H_kv * kSelCluster, threads, select_run(c.cap, threads) * (int)sizeof(uint32_t), s>>>(
-        c, lens, budget, n_sink, n_recent, kept, lens_out, dst_table, weight_out == c.weight, flags, n_flags, rows);
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               select_run(kMaxBlocks * kBlock, threads) * (int)sizeof(uint32_t));
+    if (e != cudaSuccess) return e;
+    return launch_overlapped(kernel, dim3(c.B * c.H_kv * kSelCluster), threads,
+                             select_run(c.cap, threads) * sizeof(uint32_t), s, c, lens, (int)budget, (int)n_sink,
+                             (int)n_recent, kept, lens_out, dst_table, (int)(weight_out == c.weight), flags, n_flags, rows);
   };
-  if (c.B * c.H_kv * kSelCluster <= 2 * 148) select(evict_select_kernel<1024>, 1024);
-  else select(evict_select_kernel<512>, 512);
-  if (cudaGetLastError() != cudaSuccess) return SLA_ERR_CUDA;
-  cudaLaunchConfig_t launch = {};
-  launch.gridDim = dim3((unsigned)(c.B * c.H_kv * nd));
-  launch.blockDim = dim3(kCta);
-  launch.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  launch.attrs = at;
-  launch.numAttrs = 1;
+  cudaError_t e = c.B * c.H_kv * kSelCluster <= 2 * 148 ? select(evict_select_kernel<1024>, 1024)
+                                                        : select(evict_select_kernel<512>, 512);
+  if (e != cudaSuccess) return SLA_ERR_CUDA;
   auto run = [&](auto kernel) {
-    return cudaLaunchKernelEx(&launch, kernel, c, (const int32_t*)kept, lens, (int)budget, dst_table, weight_out, flags,
-                              n_flags, (const int*)rows);
+    return launch_overlapped(kernel, dim3((unsigned)(c.B * c.H_kv * nd)), kCta, 0, s, c, (const int32_t*)kept, lens,
+                             (int)budget, dst_table, weight_out, flags, n_flags, (const int*)rows);
   };
-  cudaError_t e;
   if (c.kind == SLA_CACHE_E4M3)
     e = c.d == 128 ? run(evict_move_kernel<SLA_CACHE_E4M3, 128>) : run(evict_move_kernel<SLA_CACHE_E4M3, 64>);
   else

@@ -3,6 +3,8 @@
 #pragma once
 #include <cuda_fp16.h>
 
+#include <utility>
+
 #include "common.cuh"
 
 namespace sla {
@@ -22,6 +24,27 @@ struct CacheView {
   int B, H, H_kv, group, d, n_pages, max_blocks, cap, kind;
   float scale;
 };
+
+// Every kernel of the cache is launched so that it may start while the one before it in the
+// stream still runs (programmatic dependent launch): it sets itself up, waits for that one to
+// be complete before it touches global memory, and lets the next one start likewise.
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;"); }
+
+template <typename... P, typename... A>
+cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, A&&... args) {
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
+}
 
 sla_status check_cache(const sla_cache_config* c, const sla_cache* m, CacheView* view);
 

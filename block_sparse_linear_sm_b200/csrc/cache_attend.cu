@@ -227,8 +227,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     tc::prefetch_tensormap(&vmap);
   }
   Lines l;
+  wait_for_previous();
   scan_lines(c, a, smem + Sm::off_lines, &l, mi.warp_sums);
-  asm volatile("griddepcontrol.launch_dependents;");
+  let_next_start();
 
   // this CTA's run of the line
   const unsigned per = c.H_kv * a.groups, total = (unsigned)l.cum[c.B] * per;
@@ -645,7 +646,7 @@ __global__ void __launch_bounds__(kThreads) weight_kernel(const CacheView c, con
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   Lines l;
   scan_lines(c, a, smem, &l, warp_sums);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_for_previous();
   weigh(c, a, l, blockIdx.x * kWarps + warp, gridDim.x * kWarps, lane, nullptr, 0);
 }
 
@@ -670,7 +671,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const CacheView c, c
   const unsigned per = c.H_kv * a.groups, total = (unsigned)l.cum[c.B] * per;
   const unsigned run = a.min_run * ((total + ctas * a.min_run - 1) / (ctas * a.min_run));
   if (blockIdx.x >= segs) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    wait_for_previous();
     weigh(c, a, l, ((blockIdx.x - segs) * gridDim.y + blockIdx.y) * W + warp, (gridDim.x - segs) * gridDim.y * W, lane,
           reinterpret_cast<float*>(smem + lines_bytes(c.B)) + warp * a.rows, run);
     return;
@@ -681,8 +682,8 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const CacheView c, c
   const unsigned lo = (unsigned)l.cum[b] * per + (unsigned)sr * nb, hi = lo + nb;
   const unsigned c0 = nb ? lo / run : 0, c1 = nb ? (hi - 1) / run : 0;
   const size_t qrow = ((size_t)b * c.H + (size_t)hk * c.group) * a.T + row;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;");
+  wait_for_previous();
+  let_next_start();
   if (nb != 0 && c0 == c1) return;  // written by the CTA that had all of it
   const bool there = r < rows && row < a.rows;
   float m = -INFINITY, sum = 0.f, o[E];
@@ -777,18 +778,6 @@ sla_status plan_step(const sla_cache_config* c, int32_t T, int32_t top_n, int32_
   return SLA_OK;
 }
 
-void launch_after(cudaLaunchConfig_t* cfg, dim3 grid, int threads, size_t smem, cudaStream_t s, cudaLaunchAttribute* at) {
-  *cfg = cudaLaunchConfig_t{};
-  cfg->gridDim = grid;
-  cfg->blockDim = dim3(threads);
-  cfg->dynamicSmemBytes = smem;
-  cfg->stream = s;
-  at->id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at->val.programmaticStreamSerializationAllowed = 1;
-  cfg->attrs = at;
-  cfg->numAttrs = 1;
-}
-
 template <int KIND, int D, int NR>
 cudaError_t launch(const CacheView& c, const Step& a, int ctas, cudaStream_t s) {
   CUtensorMap kmap, vmap;
@@ -799,8 +788,7 @@ cudaError_t launch(const CacheView& c, const Step& a, int ctas, cudaStream_t s) 
   const cudaError_t e =
       cudaFuncSetAttribute(attend, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Smem<D, NR>::bytes(kCacheMaxB));
   if (e != cudaSuccess) return e;
-  attend<<<ctas, kThreads, Smem<D, NR>::bytes(c.B), s>>>(kmap, vmap, c, a);
-  return cudaGetLastError();
+  return launch_overlapped(attend, dim3(ctas), kThreads, Smem<D, NR>::bytes(c.B), s, kmap, vmap, c, a);
 }
 
 template <int KIND, int D>
@@ -821,23 +809,18 @@ cudaError_t launch_step(const CacheView& c, const Step& a, int sms, cudaStream_t
   const int ctas = per_sm * sms < kMaxCtas ? per_sm * sms : kMaxCtas;
   cudaError_t e = launch_attend(c, a, ctas, s);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg;
-  cudaLaunchAttribute at[1];
   const int segs = c.B * c.H_kv * a.groups, most = a.rows < a.group_rows ? a.rows : a.group_rows;
   // A warp a row where segments are cut into few parts, eight where one is spread over the
   // device. In the first case the weights' warps can put the parts' sums together themselves and
   // run beside the join; in the second they would each read hundreds of parts.
   if (ctas > 16 * segs) {
-    launch_after(&cfg, dim3(segs, most), kJoinThreads, lines_bytes(c.B), s, at);
-    e = cudaLaunchKernelEx(&cfg, join_kernel<D, 8>, c, a, (unsigned)ctas, segs);
+    e = launch_overlapped(join_kernel<D, 8>, dim3(segs, most), kJoinThreads, lines_bytes(c.B), s, c, a, (unsigned)ctas, segs);
     if (e != cudaSuccess || c.weight == nullptr) return e;
-    launch_after(&cfg, dim3(8 * sms), kThreads, lines_bytes(c.B), s, at);
-    return cudaLaunchKernelEx(&cfg, weight_kernel, c, a);
+    return launch_overlapped(weight_kernel, dim3(8 * sms), kThreads, lines_bytes(c.B), s, c, a);
   }
   const int y = (most + 7) / 8, more = c.weight != nullptr ? (4 * sms + y - 1) / y : 0;
   const size_t smem = lines_bytes(c.B) + (c.weight != nullptr ? kJoinThreads / 32 * a.rows * sizeof(float) : 0);
-  launch_after(&cfg, dim3(segs + more, y), kJoinThreads, smem, s, at);
-  return cudaLaunchKernelEx(&cfg, join_kernel<D, 1>, c, a, (unsigned)ctas, segs);
+  return launch_overlapped(join_kernel<D, 1>, dim3(segs + more, y), kJoinThreads, smem, s, c, a, (unsigned)ctas, segs);
 }
 
 }  // namespace

@@ -585,8 +585,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::prefetch_tensormap(&vmap);
   }
   Lines l;
+  wait_for_previous();
   scan_lines(c, a, smem + Sm::off_lines, &l, mi.warp_sums);
-  asm volatile("griddepcontrol.launch_dependents;");
+  let_next_start();
   const unsigned per = c.H_kv * a.groups, total = (unsigned)l.cum[c.B] * per;
   const unsigned run = a.min_run * ((total + gridDim.x * a.min_run - 1) / (gridDim.x * a.min_run));
   const unsigned lo = min(total, blockIdx.x * run), hi = min(total, lo + run);
@@ -641,8 +642,7 @@ cudaError_t launch(const CacheView& c, const Step& a, int ctas, cudaStream_t s) 
   const cudaError_t e =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Smem<D>::bytes(kCacheMaxB));
   if (e != cudaSuccess) return e;
-  kernel<<<ctas, kThreads, Smem<D>::bytes(c.B), s>>>(kmap, vmap, c, a);
-  return cudaGetLastError();
+  return launch_overlapped(kernel, dim3(ctas), kThreads, Smem<D>::bytes(c.B), s, kmap, vmap, c, a);
 }
 
 }  // namespace

@@ -74,6 +74,8 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 4)
   const int bh = blockIdx.x / kCluster, b = bh / c.H_kv, hk = bh % c.H_kv;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t rank = cluster_rank();
+  wait_for_previous();
+  let_next_start();
   bool bad = false;
   const int L = checked_len(lens, b, c.cap, &bad), nq = checked_new(n_new, b, T, &bad);
   if (bad && tid == 0 && hk == 0 && rank == 0) report(c.status, SLA_ERR_DEVICE_CHECK, kDetailCacheLen);
@@ -271,9 +273,10 @@ extern "C" sla_status sla_cache_route(const void* q, const sla_cache_config* cfg
   auto run = [&](auto kernel) {
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes(kMaxBlocks)) != cudaSuccess)
       return SLA_ERR_CUDA;
-    kernel<<<c.B * c.H_kv * kCluster, kThreads, bytes(c.max_blocks), (cudaStream_t)stream>>>(
-        c, (const __nv_bfloat16*)q, T, lens, n_new, top_n, sel);
-    return cudaGetLastError() == cudaSuccess ? SLA_OK : SLA_ERR_CUDA;
+    const cudaError_t e = launch_overlapped(kernel, dim3(c.B * c.H_kv * kCluster), kThreads, bytes(c.max_blocks),
+                                            (cudaStream_t)stream, c, (const __nv_bfloat16*)q, (int)T, lens, n_new,
+                                            (int)top_n, sel);
+    return e == cudaSuccess ? SLA_OK : SLA_ERR_CUDA;
   };
   return c.d == 128 ? run(route_kernel<128>) : run(route_kernel<64>);
 }
