@@ -33,8 +33,11 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  cluster_arrive();
+  cluster_wait();
 }
 __device__ __forceinline__ uint32_t peer_addr(const void* p, uint32_t rank) {
   uint32_t a;
@@ -85,6 +88,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 4)
     if (rank == 0 && tid < top_n) out[tid] = -1;
     return;
   }
+  cluster_arrive();  // a CTA's shared memory may be written from when it has started: waited for below
   const int run = route_run(n), j0 = min(n, (int)rank * run), mine = min(n, j0 + run) - j0;
   const int pitch = run + 1;
   double *score = dyn, *sum = dyn + kHeads * pitch;
@@ -159,6 +163,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 4)
       }
     }
     __syncthreads();
+    if (h0 == 0) cluster_wait();
     // a warp two heads: this CTA's maximum, to every CTA
     for (int h = warp; h < heads; h += kWarps) {
       double t = -INFINITY;
