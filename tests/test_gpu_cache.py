@@ -800,6 +800,50 @@ def test_streams_and_captured_steps():
     p.status()
 
 
+def test_captured_beside_copies_and_a_second_stream():
+    """Copies before, between and behind the calls, and the routing on a stream of its own that
+    the attention waits for: each call sees what was written before it, replay after replay."""
+    p = Pair(B=2, H=8, H_kv=2, d=64, max_blocks=8, seed=61)
+    p.fill([200, 77])
+    c, T = p.cfg, 2
+    k, v, q = *p.kv(T), p.queries(T)
+    k_in, v_in, q_in = torch.empty_like(k), torch.empty_like(v), torch.empty_like(q)
+    lens, new_lens, lens_b = i32(p.lens), i32(p.lens), i32(p.lens)
+    sel, sel_b = (torch.zeros(2, 2, 3, dtype=torch.int32, device="cuda") for _ in range(2))
+    out, out_b = torch.empty_like(q), torch.empty_like(q)
+    ws = torch.empty(sla.sla_cache_attend_workspace_bytes(c, T, 3, 64, True), dtype=torch.uint8, device="cuda")
+    side, other = torch.cuda.Stream(), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        k_in.copy_(k)
+        v_in.copy_(v)
+        sla.sla_cache_append(k_in, v_in, c, p.c, lens, None, new_lens)
+        lens_b.copy_(new_lens)
+        other.wait_stream(side)
+        with torch.cuda.stream(other):
+            q_in.copy_(q)
+            sla.sla_cache_route(q_in, c, p.c, lens_b, None, sel)
+            sel_b.copy_(sel)
+        lens.copy_(new_lens)
+        side.wait_stream(other)
+        sla.sla_cache_attend(q_in, c, p.c, lens_b, None, sel_b, 64, out, ws)
+        out_b.copy_(out)
+    for step in range(20):
+        nk, nv = p.kv(T)
+        nq = p.queries(T)
+        k.copy_(nk), v.copy_(nv), q.copy_(nq)
+        g.replay()
+        p.lens = p.o.append(f64(nk), f64(nv), p.lens, [T, T])
+        want_sel, gap = p.o.route(f64(nq), p.lens, [T, T], 3)
+        assert gap > 1e-9
+        np.testing.assert_array_equal(sel_b.cpu().numpy(), want_sel)
+        want, mag, _ = p.o.attend(f64(nq), p.lens, [T, T], want_sel, 64)
+        assert np.all(np.abs(f64(out_b) - want) <= 2.0 ** -8 * np.abs(want) + (2.0 ** -11 + 2.0 ** -16) * mag)
+    assert lens.tolist() == p.lens.tolist()
+    p.status()
+
+
 def test_calls_on_a_given_stream():
     """stream= instead of the current one: ordered with work on that stream only."""
     p = Pair(B=2, H=4, H_kv=2, d=64, max_blocks=4, seed=61)
