@@ -154,9 +154,9 @@ __device__ __forceinline__ void write_mean(const uint8_t* tile, float scale, flo
 // A thread holds its 16-element chunks as the bf16 words that it loaded (8 registers) and
 // takes the largest magnitude on their bits, which order like the magnitudes. One pass: a page
 // is read, its scale found with one barrier, and written. Bound by HBM for prompts (2 x 12 x
-// 32760 rows of 128, int8: 79 us on the device, 6.0 TB/s of the 476 MB it cannot do without),
+// 32760 rows of 128, int8: 80 us on the device, 5.9 TB/s of the 476 MB it cannot do without),
 // by its chain of loads (length, page, rows, barrier) for a step's one token (64 sequences x 8
-// heads: 5.4 us).
+// heads: 6 us).
 // ---------------------------------------------------------------------------
 template <int KIND, int D>
 __global__ void __launch_bounds__(kCta) append_kernel(const CacheView c, const __nv_bfloat16* __restrict__ k_new,

@@ -26,11 +26,11 @@
 // movmatrix turns P's 8 x 8 pieces into the second product's operand.
 //
 // What bounds it. A large batch: HBM (64 sequences of up to 16384 tokens, 8 KV heads, 4 rows
-// each: 194 us on the device for 1.25 GB, 6.4 TB/s, 0.98 of the measured copy rate; with the
+// each: 189 us on the device for 1.25 GB, 6.6 TB/s, the measured copy rate; with the
 // rows as the 16-row operand, 4 rows padded to 16, it was 240). A few sequences: latency. A
 // warp's tile takes some 4000 cycles (products 1300 and 1500, softmax 1000), and 296 CTAs leave
 // it three or four tiles behind a start of 3 us (lengths, table, page): 65536 tokens of one
-// sequence, 16 rows, 21 us. More than 16 rows read a page once a group of 16, from L2: 128 rows
+// sequence, 16 rows, 20 us. More than 16 rows read a page once a group of 16, from L2: 128 rows
 // were bound by that (5.9 TB/s of L2 reads), hence the other kernel. Twelve warps an SM instead
 // of eight, at 168 registers, were 12 % slower.
 #include <cuda.h>
@@ -656,7 +656,7 @@ __global__ void __launch_bounds__(kThreads) weight_kernel(const CacheView c, con
 // PW warps a row take the partials in turn, a lane D / 32 columns; a CTA has 8 / PW rows. CTAs
 // behind the segments' add the weights meanwhile. Launched while the attention kernel runs
 // (programmatic dependent launch), so that only its loads wait. Bound by their latency: 4 to 8
-// us, the longer for the 74 parts of a segment spread over the device.
+// us, the longer for the 64 parts of a segment spread over the device.
 constexpr int kJoinThreads = 256;
 
 template <int D, int PW>
