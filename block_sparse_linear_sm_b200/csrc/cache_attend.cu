@@ -141,7 +141,7 @@ __device__ __forceinline__ void look_ahead(Ring<D>& r, const CacheView& c, const
         r.list[lane] = e;
       }
       const int2 e = r.list[lane];
-      j = listed_block(a, r.idx, first, e.x, e.y, &chosen);
+      j = listed_block(a, r.idx, l.len[r.b], first, lane, e.x, e.y, &chosen);
     }
     if (j >= 0) {
       r.ahead.seg = r.seg;
@@ -621,16 +621,20 @@ __device__ void weigh(const CacheView& c, const Step& a, const Lines& l, unsigne
     const float4* s = reinterpret_cast<const float4*>(a.scores + ((size_t)t * kBlock + lane) * a.score_rows);
     const int half = 32 * a.score_rows / 4;  // from slot lane to slot lane + 32
     float x = 0.f, y = 0.f;
-    for (int r = 0; r < a.rows; r += 4) {
-      const float4 u = s[r / 4], v = s[r / 4 + half];
-      const float us[4] = {u.x, u.y, u.z, u.w}, vs[4] = {v.x, v.y, v.z, v.w};
+    int token = 0;  // of the row's T
+#pragma unroll 2
+    for (int r = 0; r < a.score_rows; r += 8) {
+      const float4 u0 = s[r / 4], u1 = s[r / 4 + 1], v0 = s[r / 4 + half], v1 = s[r / 4 + 1 + half];
+      const float us[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
+      const float vs[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float z = r + e < a.rows && (a.T == 1 || (r + e) % a.T < n) ? row_lse[r + e] : -INFINITY;
+      for (int e = 0; e < 8; ++e) {
+        const float z = r + e < a.rows && token < n ? row_lse[r + e] : -INFINITY;
         if (z > -INFINITY) {  // neither a row that sees nothing nor one that is NaN
           x += tc::ex2_approx(us[e] - z);
           y += tc::ex2_approx(vs[e] - z);
         }
+        token = token + 1 == a.T ? 0 : token + 1;
       }
     }
     float* w = c.weight + ((size_t)b * c.H_kv + hk) * c.cap + j * kBlock + lane;

@@ -29,14 +29,16 @@ struct Step {
 // ---------------------------------------------------------------------------
 // the line of tiles
 // ---------------------------------------------------------------------------
-// Tiles of one (sequence, KV head): list entries first, then the window's (or all) blocks.
+// Tiles of one (sequence, KV head): the list's valid entries first, as many as there can be in
+// a list of top_n and a sequence of L, then the window's (or all) blocks.
+__device__ __forceinline__ int listed_tiles(const Step& a, int L) { return min(a.top_n, (L + kBlock - 1) / kBlock); }
 __device__ __forceinline__ int first_block(const Step& a, int L, int n) {
   return a.window > 0 ? max(0, L - n - a.window + 1) / kBlock : 0;
 }
 __device__ __forceinline__ int tile_count(const Step& a, int L, int n) {
   if (n == 0 || L == 0) return 0;
   const int range = (L + kBlock - 1) / kBlock - first_block(a, L, n);
-  return a.sel == nullptr ? range : a.top_n + (a.window > 0 ? range : 0);
+  return a.sel == nullptr ? range : listed_tiles(a, L) + (a.window > 0 ? range : 0);
 }
 
 struct Lines {  // in shared memory
@@ -127,10 +129,19 @@ __device__ __forceinline__ void valid_entries(const CacheView& c, const Step& a,
 
 // Block of tile idx of a sequence whose list's valid entries the warp holds; -1 where it is
 // none. *chosen: the window does not limit it.
-__device__ __forceinline__ int listed_block(const Step& a, int idx, int first, int e0, int e1, bool* chosen) {
-  *chosen = idx < a.top_n;
-  if (idx < a.top_n) return __shfl_sync(0xffffffffu, idx < 32 ? e0 : e1, idx & 31);
-  const int j = first + idx - a.top_n;
+__device__ __forceinline__ int listed_block(const Step& a, int idx, int L, int first, int lane, int e0, int e1,
+                                            bool* chosen) {
+  const int listed = listed_tiles(a, L);
+  *chosen = idx < listed;
+  if (idx < listed) {  // the valid entry that idx of them are before
+    const uint32_t m0 = __ballot_sync(0xffffffffu, e0 >= 0), m1 = __ballot_sync(0xffffffffu, e1 >= 0);
+    const bool late = idx >= __popc(m0);
+    const int e = late ? e1 : e0;
+    const int before = late ? __popc(m0) + __popc(m1 & ((1u << lane) - 1)) : __popc(m0 & ((1u << lane) - 1));
+    const uint32_t hit = __ballot_sync(0xffffffffu, e >= 0 && before == idx);
+    return hit == 0 ? -1 : __shfl_sync(0xffffffffu, e, __ffs(hit) - 1);
+  }
+  const int j = first + idx - listed;
   return __any_sync(0xffffffffu, e0 == j || e1 == j) ? -1 : j;
 }
 
@@ -144,7 +155,7 @@ __device__ __forceinline__ int tile_block(const CacheView& c, const Step& a, int
   }
   int e0, e1;
   valid_entries(c, a, b, hk, L, lane, e0, e1);
-  return listed_block(a, idx, first, e0, e1, chosen);
+  return listed_block(a, idx, L, first, lane, e0, e1, chosen);
 }
 
 // A segment of the line: one row group of one KV head of one sequence, with its tiles.

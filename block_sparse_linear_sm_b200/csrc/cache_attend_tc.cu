@@ -110,24 +110,23 @@ __device__ int lane_block(const CacheView& c, const Step& a, int b, int hk, int 
   *chosen = a.window == 0;
   if (a.sel == nullptr) return first + idx;
   const int32_t* list = a.sel + ((size_t)b * c.H_kv + hk) * a.top_n;
-  int top = -1;
-  if (idx < a.top_n) {
-    *chosen = true;
-    for (int i = 0; i < idx; ++i) top = max(top, list[i]);
-    const int e = list[idx];
-    if (e < 0) return -1;
-    if (e > top && e < (L + kBlock - 1) / kBlock) return e;
-    report(c.status, SLA_ERR_DEVICE_CHECK, kDetailCacheSel);
-    return -1;
-  }
-  *chosen = false;
-  const int j = first + idx - a.top_n;
+  const int listed = listed_tiles(a, L), j = first + idx - listed, blocks = (L + kBlock - 1) / kBlock;
+  int top = -1, valid = 0, entry = -1;  // entry: the valid one that idx of them are before
+  bool bad = false, twice = false;      // twice: j is in the list
   for (int i = 0; i < a.top_n; ++i) {
     const int e = list[i];
-    if (e == j && e > top) return -1;
+    if (e > top && e < blocks) {
+      if (valid++ == idx) entry = e;
+      if (e == j) twice = true;
+    } else if (e >= 0) {
+      bad = true;
+    }
     top = max(top, e);
   }
-  return j;
+  if (bad) report(c.status, SLA_ERR_DEVICE_CHECK, kDetailCacheSel);
+  *chosen = idx < listed;
+  if (*chosen) return entry;
+  return twice ? -1 : j;
 }
 
 // ---------------------------------------------------------------------------

@@ -300,6 +300,32 @@ def test_attend_selected_blocks(window, T, H, kind):
         assert not out[2].any()   # no block, no window
 
 
+@pytest.mark.parametrize("window", [0, 100])
+@pytest.mark.parametrize("T,H", [(1, 4), (3, 32), (5, 32)])
+def test_attend_lists_longer_than_the_sequence(window, T, H):
+    """64 entries, anywhere between the -1, of which the valid ones are few."""
+    p = Pair(B=4, H=H, H_kv=2, d=64, max_blocks=40, seed=window + H)
+    p.fill([40 * 64, 200, 64, 5])
+    rng = np.random.default_rng(T)
+    sel = np.full((4, 2, 64), -1, np.int32)
+    for b, n in enumerate((40, 4, 1, 1)):
+        for hk in range(2):
+            keep = np.sort(rng.permutation(n)[:max(1, n - 3 * hk)])
+            sel[b, hk, np.sort(rng.permutation(64)[:len(keep)])] = keep
+    sel[1, 0] = -1
+    sel[1, 0, [0, 31, 32, 63]] = [0, 1, 2, 3]
+    q = p.queries(T)
+    out = p.check_attend(q, sel=sel, window=window)
+    for bad in ([0, 31, 33, 63], [0, 1, 2, 3]):   # an entry too large behind the last valid one
+        sel[1, 0] = -1
+        sel[1, 0, bad] = [0, 1, 2, 3]
+        sel[1, 0, 40 if bad[2] == 2 else 62] = 3
+        sel[1, 0, 63] = 4
+        got = p.attend(q, sel=sel, window=window, weight=False)
+        p.status((sla.SLA_ERR_DEVICE_CHECK, 112))
+        assert torch.equal(got, out)
+
+
 @pytest.mark.parametrize("T,H", [(1, 4), (6, 16)])
 def test_attend_longest_list(T, H):
     p = Pair(B=1, H=H, H_kv=1, d=64, max_blocks=70, seed=9)
