@@ -35,6 +35,8 @@
 // of eight, at 168 registers, were 12 % slower.
 #include <cuda.h>
 
+#include <algorithm>
+
 #include "cache_attend.cuh"
 
 namespace sla {
@@ -233,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 
   // this CTA's run of the line
   const unsigned per = c.H_kv * a.groups, total = (unsigned)l.cum[c.B] * per;
-  const unsigned run = a.min_run * ((total + gridDim.x * a.min_run - 1) / (gridDim.x * a.min_run));
+  const unsigned run = run_length(a, total, c.B * per, gridDim.x);
   const unsigned lo = min(total, blockIdx.x * run), hi = min(total, lo + run);
   if (lo >= hi) return;
 
@@ -583,14 +585,19 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 // ---------------------------------------------------------------------------
 // weights: weight[b, hk, s] += sum over rows of 2^(score - lse), rows in order
 // ---------------------------------------------------------------------------
-// Warp `first` of `step`: a warp a tile (list entries that name no block are passed over), a
-// lane two slots. lse: this warp's log2-sum-exp of the tile's rows, put together from the
-// parts of its segments (run: tiles of a part); null: a.lse has them.
-__device__ void weigh(const CacheView& c, const Step& a, const Lines& l, unsigned first, unsigned step, int lane,
-                      float* lse, unsigned run) {
+// A CTA of `ctas` takes an equal run of the tiles, which are few: a CTA's warps wait for one
+// another's loads of scores (a slot's rows are a line), yet share the parts of their rows. A
+// warp a tile (list entries that name no block are passed over), a lane two slots. lse: this warp's place for the log2-sum-exp of the tile's rows, put together
+// from the parts of its segments (run: tiles of a part), or taken from a.lse where run is 0;
+// infinite for rows that add nothing. Bound by the chain of loads (8 sequences of up to 8191
+// tokens, 4 KV heads, 16 rows: 5 to 8 us beside the join): what can start before the rows'
+// sums does.
+__device__ void weigh(const CacheView& c, const Step& a, const Lines& l, unsigned cta, unsigned ctas, unsigned warp,
+                      unsigned warps, int lane, float* lse, unsigned run) {
   const unsigned per = c.H_kv, total = (unsigned)l.cum[c.B] * per;
   int have = -1;  // (sequence, KV head) whose rows lse holds
-  for (unsigned t = first; t < total; t += step) {
+  const unsigned mine = (total + ctas - 1) / ctas, end = min(total, (cta + 1) * mine);
+  for (unsigned t = cta * mine + warp; t < end; t += warps) {
     const int b = find_sequence(l, c.B, t, per), nb = l.cum[b + 1] - l.cum[b], L = l.len[b], n = l.fresh[b];
     const unsigned in = t - (unsigned)l.cum[b] * per;
     const int hk = (int)(in / (unsigned)nb);
@@ -598,30 +605,39 @@ __device__ void weigh(const CacheView& c, const Step& a, const Lines& l, unsigne
     const int j = tile_block(c, a, b, hk, (int)(in - (unsigned)hk * nb), L, n, lane, &chosen);
     if (j < 0) continue;
     const int page = c.table[(size_t)b * c.max_blocks + j];
-    if (page < 0 || page >= c.n_pages) continue;  // reported by the attention kernel
-    const float* row_lse = lse != nullptr ? lse : a.lse + ((size_t)b * c.H + (size_t)hk * c.group) * a.T;
-    if (lse != nullptr && have != b * c.H_kv + hk) {
+    float* w = c.weight + ((size_t)b * c.H_kv + hk) * c.cap + j * kBlock + lane;
+    const bool live0 = j * kBlock + lane < L, live1 = j * kBlock + lane + 32 < L;
+    const float w0 = live0 ? w[0] : 0.f, w1 = live1 ? w[32] : 0.f;
+    if (have != b * c.H_kv + hk) {
       have = b * c.H_kv + hk;
       __syncwarp();
-      for (int r = lane; r < a.rows; r += 32) {
-        const int grp = r / a.group_rows, seg = have * a.groups + grp, at = r - grp * a.group_rows;
-        const unsigned lo = (unsigned)l.cum[b] * per * a.groups + (unsigned)(hk * a.groups + grp) * nb;
-        float m = -INFINITY, sum = 0.f;
+      for (int r = lane; r < a.score_rows; r += 32) {
+        float z = -INFINITY;
+        if (r < a.rows && r % a.T < n) {
+          if (run == 0) {
+            z = a.lse[((size_t)b * c.H + (size_t)hk * c.group) * a.T + r];
+          } else {
+            const int grp = r / a.group_rows, seg = have * a.groups + grp, at = r - grp * a.group_rows;
+            const unsigned lo = (unsigned)l.cum[b] * per * a.groups + (unsigned)(hk * a.groups + grp) * nb;
+            float m = -INFINITY, sum = 0.f;
 #pragma unroll 4
-        for (unsigned i = lo / run; i <= (lo + nb - 1) / run; ++i) {
-          const float* ml = a.part_ml + ((size_t)i + seg) * 2 * a.group_rows + at;
-          const float x = ml[0], y = ml[a.group_rows], next = fmaxf(m, x), base = next == -INFINITY ? 0.f : next;
-          sum = sum * tc::ex2_approx(m - base) + y * tc::ex2_approx(x - base);
-          m = next;
+            for (unsigned i = lo / run; i <= (lo + nb - 1) / run; ++i) {
+              const float* ml = a.part_ml + ((size_t)i + seg) * 2 * a.group_rows + at;
+              const float x = ml[0], y = ml[a.group_rows], next = fmaxf(m, x), base = next == -INFINITY ? 0.f : next;
+              sum = sum * tc::ex2_approx(m - base) + y * tc::ex2_approx(x - base);
+              m = next;
+            }
+            z = log2_sum(m, sum);
+          }
         }
-        lse[r] = log2_sum(m, sum);
+        lse[r] = z > -INFINITY ? z : INFINITY;  // neither a row that sees nothing nor one that is NaN
       }
       __syncwarp();
     }
+    if (page < 0 || page >= c.n_pages) continue;  // reported by the attention kernel
     const float4* s = reinterpret_cast<const float4*>(a.scores + ((size_t)t * kBlock + lane) * a.score_rows);
     const int half = 32 * a.score_rows / 4;  // from slot lane to slot lane + 32
     float x = 0.f, y = 0.f;
-    int token = 0;  // of the row's T
 #pragma unroll 2
     for (int r = 0; r < a.score_rows; r += 8) {
       const float4 u0 = s[r / 4], u1 = s[r / 4 + 1], v0 = s[r / 4 + half], v1 = s[r / 4 + 1 + half];
@@ -629,17 +645,13 @@ __device__ void weigh(const CacheView& c, const Step& a, const Lines& l, unsigne
       const float vs[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float z = r + e < a.rows && token < n ? row_lse[r + e] : -INFINITY;
-        if (z > -INFINITY) {  // neither a row that sees nothing nor one that is NaN
-          x += tc::ex2_approx(us[e] - z);
-          y += tc::ex2_approx(vs[e] - z);
-        }
-        token = token + 1 == a.T ? 0 : token + 1;
+        const float z = lse[r + e];
+        x += z < INFINITY ? tc::ex2_approx(us[e] - z) : 0.f;
+        y += z < INFINITY ? tc::ex2_approx(vs[e] - z) : 0.f;
       }
     }
-    float* w = c.weight + ((size_t)b * c.H_kv + hk) * c.cap + j * kBlock + lane;
-    if (j * kBlock + lane < L) *w += x;
-    if (j * kBlock + lane + 32 < L) w[32] += y;
+    if (live0) w[0] = w0 + x;
+    if (live1) w[32] = w1 + y;
   }
 }
 
@@ -651,14 +663,15 @@ __global__ void __launch_bounds__(kThreads) weight_kernel(const CacheView c, con
   Lines l;
   scan_lines(c, a, smem, &l, warp_sums);
   wait_for_previous();
-  weigh(c, a, l, blockIdx.x * kWarps + warp, gridDim.x * kWarps, lane, nullptr, 0);
+  weigh(c, a, l, blockIdx.x, gridDim.x, warp, kWarps, lane,
+        reinterpret_cast<float*>(smem + lines_bytes(c.B)) + warp * a.score_rows, 0);
 }
 
 // ---------------------------------------------------------------------------
 // segments that several CTAs worked on, or none
 // ---------------------------------------------------------------------------
 // PW warps a row take the partials in turn, a lane D / 32 columns; a CTA has 8 / PW rows. CTAs
-// behind the segments' add the weights meanwhile. Launched while the attention kernel runs
+// before the segments' add the weights, whose chain is the longer one. Launched while the attention kernel runs
 // (programmatic dependent launch), so that only its loads wait. Bound by their latency: 4 to 8
 // us, the longer for the 64 parts of a segment spread over the device.
 constexpr int kJoinThreads = 256;
@@ -673,14 +686,15 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const CacheView c, c
   Lines l;
   scan_lines(c, a, smem, &l, warp_sums);
   const unsigned per = c.H_kv * a.groups, total = (unsigned)l.cum[c.B] * per;
-  const unsigned run = a.min_run * ((total + ctas * a.min_run - 1) / (ctas * a.min_run));
-  if (blockIdx.x >= segs) {
+  const unsigned run = run_length(a, total, c.B * per, ctas);
+  const int weighing = gridDim.x - segs;
+  if (blockIdx.x < weighing) {
     wait_for_previous();
-    weigh(c, a, l, ((blockIdx.x - segs) * gridDim.y + blockIdx.y) * W + warp, (gridDim.x - segs) * gridDim.y * W, lane,
-          reinterpret_cast<float*>(smem + lines_bytes(c.B)) + warp * a.rows, run);
+    weigh(c, a, l, blockIdx.x * gridDim.y + blockIdx.y, weighing * gridDim.y, warp, W, lane,
+          reinterpret_cast<float*>(smem + lines_bytes(c.B)) + warp * a.score_rows, run);
     return;
   }
-  const int rows = a.group_rows, seg = blockIdx.x, b = seg / (int)per, sr = seg % (int)per, hk = sr / a.groups;
+  const int rows = a.group_rows, seg = blockIdx.x - weighing, b = seg / (int)per, sr = seg % (int)per, hk = sr / a.groups;
   const int r = blockIdx.y * (W / PW) + warp / PW, row = sr % a.groups * rows + r;
   const int nb = l.cum[b + 1] - l.cum[b];
   const unsigned lo = (unsigned)l.cum[b] * per + (unsigned)sr * nb, hi = lo + nb;
@@ -745,6 +759,7 @@ constexpr int kMaxCtas = kCtasPerSm * 148;  // a workspace is sized for this gri
 
 struct Layout {
   size_t ml, o, lse, scores, total;
+  int64_t tiles;  // at most, of all KV heads
   int rows, group_rows, groups;
 };
 
@@ -765,7 +780,7 @@ sla_status plan_step(const sla_cache_config* c, int32_t T, int32_t top_n, int32_
   p->group_rows = p->rows <= 8 ? 8 : p->rows <= kFewRows ? 16 : kTcGroupRows;
   p->groups = (p->rows + p->group_rows - 1) / p->group_rows;
   const int64_t segs = (int64_t)c->B * c->H_kv * p->groups;
-  const int64_t tiles = (int64_t)c->B * c->H_kv * most_tiles(c, T, top_n, window);
+  const int64_t tiles = p->tiles = (int64_t)c->B * c->H_kv * most_tiles(c, T, top_n, window);
   if (tiles * p->groups >= ((int64_t)1 << 31)) return SLA_ERR_UNSUPPORTED;  // the line is counted in 32 bits
   size_t off = 0;
   auto take = [&](size_t bytes) {
@@ -808,22 +823,24 @@ cudaError_t launch_attend(const CacheView& c, const Step& a, int ctas, cudaStrea
 }
 
 template <int D>
-cudaError_t launch_step(const CacheView& c, const Step& a, int sms, cudaStream_t s) {
+cudaError_t launch_step(const CacheView& c, const Step& a, int sms, int64_t tiles, cudaStream_t s) {
   const int per_sm = a.group_rows == kTcGroupRows ? 1 : kCtasPerSm;
   const int ctas = per_sm * sms < kMaxCtas ? per_sm * sms : kMaxCtas;
   cudaError_t e = launch_attend(c, a, ctas, s);
   if (e != cudaSuccess) return e;
   const int segs = c.B * c.H_kv * a.groups, most = a.rows < a.group_rows ? a.rows : a.group_rows;
+  const int weighing = (int)std::min<int64_t>((c.weight != nullptr ? 4 : 0) * sms, tiles);
   // A warp a row where segments are cut into few parts, eight where one is spread over the
   // device. In the first case the weights' warps can put the parts' sums together themselves and
   // run beside the join; in the second they would each read hundreds of parts.
   if (ctas > 16 * segs) {
     e = launch_overlapped(join_kernel<D, 8>, dim3(segs, most), kJoinThreads, lines_bytes(c.B), s, c, a, (unsigned)ctas, segs);
     if (e != cudaSuccess || c.weight == nullptr) return e;
-    return launch_overlapped(weight_kernel, dim3(8 * sms), kThreads, lines_bytes(c.B), s, c, a);
+    return launch_overlapped(weight_kernel, dim3(weighing), kThreads,
+                            lines_bytes(c.B) + kWarps * a.score_rows * sizeof(float), s, c, a);
   }
-  const int y = (most + 7) / 8, more = c.weight != nullptr ? (4 * sms + y - 1) / y : 0;
-  const size_t smem = lines_bytes(c.B) + (c.weight != nullptr ? kJoinThreads / 32 * a.rows * sizeof(float) : 0);
+  const int y = (most + 7) / 8, more = (weighing + y - 1) / y;
+  const size_t smem = lines_bytes(c.B) + (c.weight != nullptr ? kJoinThreads / 32 * a.score_rows * sizeof(float) : 0);
   return launch_overlapped(join_kernel<D, 1>, dim3(segs + more, y), kJoinThreads, smem, s, c, a, (unsigned)ctas, segs);
 }
 
@@ -870,12 +887,12 @@ sla_status sla_cache_attend(const void* q, const sla_cache_config* cfg, const sl
   a.rows = p.rows;
   a.groups = p.groups;
   a.group_rows = p.group_rows;
-  a.min_run = p.group_rows == kTcGroupRows ? 1 : kWarps;
+  a.round = p.group_rows == kTcGroupRows ? 1 : kWarps;
   a.score_rows = (int)align_up(p.rows, 8);
   const int sms = sm_count();
   if (sms < 1) return SLA_ERR_CUDA;
   cudaStream_t s = (cudaStream_t)stream;
-  const cudaError_t e = c.d == 128 ? launch_step<128>(c, a, sms, s) : launch_step<64>(c, a, sms, s);
+  const cudaError_t e = c.d == 128 ? launch_step<128>(c, a, sms, p.tiles, s) : launch_step<64>(c, a, sms, p.tiles, s);
   return e == cudaSuccess ? SLA_OK : SLA_ERR_CUDA;
 }
 

@@ -22,7 +22,7 @@ struct Step {
   float* scores;    // [tiles of all (sequence, KV head)][64][score_rows] (with weights)
   int T, top_n, window, rows, groups;  // rows = T * group of a KV head, in groups of group_rows
   int group_rows;
-  unsigned min_run;                    // tiles a CTA takes at least
+  unsigned round;                      // tiles that a CTA works on at once
   int score_rows;                      // rows rounded up to 8
 };
 
@@ -86,6 +86,14 @@ static __device__ void scan_lines(const CacheView& c, const Step& a, char* smem,
   if (b0 < c.B && b0 + per >= c.B) l.cum[c.B] = before;
   __syncthreads();
   *out = l;
+}
+
+// Tiles a CTA's run has. Whole rounds leave fewer parts to join; where segments (segs of them)
+// are shorter than a round, it counts as no longer than they are on average: a CTA's segments
+// come one after another, and 432 of one tile each would else keep 108 of 296 CTAs busy.
+__device__ __forceinline__ unsigned run_length(const Step& a, unsigned total, unsigned segs, unsigned ctas) {
+  const unsigned unit = max(1u, min(a.round, total / segs));
+  return unit * ((total + ctas * unit - 1) / (ctas * unit));
 }
 
 // Sequence that holds tile t of the line (per: segments a KV-head line of a sequence has).

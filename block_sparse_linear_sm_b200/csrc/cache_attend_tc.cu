@@ -588,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   scan_lines(c, a, smem + Sm::off_lines, &l, mi.warp_sums);
   let_next_start();
   const unsigned per = c.H_kv * a.groups, total = (unsigned)l.cum[c.B] * per;
-  const unsigned run = a.min_run * ((total + gridDim.x * a.min_run - 1) / (gridDim.x * a.min_run));
+  const unsigned run = run_length(a, total, c.B * per, gridDim.x);
   const unsigned lo = min(total, blockIdx.x * run), hi = min(total, lo + run);
   if (lo >= hi) return;
   if (warp == 1) {
