@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(kCta) append_kernel(const CacheView c, const _
 }
 
 // ---------------------------------------------------------------------------
-// evict, first step: which slots stay (one cluster of eight CTAs a sequence and KV head)
+// evict, first step: which slots stay (one cluster of eight CTAs a sequence and KV head, or one CTA)
 //
 // The budget - n_sink - n_recent heaviest of the slots between are those above a threshold
 // weight and the first few equal to it. Each CTA keeps its eighth of the weights in shared
@@ -276,7 +276,6 @@ __global__ void __launch_bounds__(kCta) append_kernel(const CacheView c, const _
 // digits of a pass, a cluster barrier and a scan each), not by the 4 bytes a slot: 65536 slots
 // of 4 heads 19 us, up to 16384 of 64 heads 21 us.
 // ---------------------------------------------------------------------------
-constexpr int kSelCluster = 8;
 
 __device__ __forceinline__ uint32_t weight_key(float w) {
   if (isnan(w)) w = -INFINITY;
@@ -300,12 +299,14 @@ __device__ __forceinline__ int peer_int(const int* p, uint32_t rank) {
   return v;
 }
 
+constexpr int kSelAlone = 8192;  // slots that one CTA takes by itself at most
+
 // Slots of one CTA's run: a multiple of 32 a warp.
-__host__ __device__ inline int select_run(int n, int threads) {
-  return (int)align_up((size_t)(n + kSelCluster - 1) / kSelCluster, threads);
+__host__ __device__ inline int select_run(int n, int ctas, int threads) {
+  return (int)align_up((size_t)(n + ctas - 1) / ctas, threads);
 }
 
-template <int kSelThreads>
+template <int kSelCluster, int kSelThreads>
 __global__ void __cluster_dims__(kSelCluster, 1, 1) __launch_bounds__(kSelThreads)
     evict_select_kernel(const CacheView c, const int32_t* __restrict__ lens, int budget, int n_sink, int n_recent,
                         int32_t* __restrict__ kept, int32_t* lens_out, const int32_t* __restrict__ dst_table,
@@ -354,7 +355,7 @@ __global__ void __cluster_dims__(kSelCluster, 1, 1) __launch_bounds__(kSelThread
     return;
   }
   const float* w = c.weight + (size_t)bh * c.cap;
-  const int run = select_run(n, kSelThreads), a = min(n, rank * run), z = min(n, a + run);
+  const int run = select_run(n, kSelCluster, kSelThreads), a = min(n, rank * run), z = min(n, a + run);
   const int lo = n_sink, hi = n - n_recent;    // n_sink + n_recent <= budget < n: lo < hi
   const int want = budget - n_sink - n_recent;  // of the slots between
   for (int i = a + tid; i < z; i += kSelThreads) keys[i - a] = weight_key(w[i]);
@@ -676,17 +677,23 @@ sla_status sla_cache_evict(const sla_cache_config* cfg, const sla_cache* cache, 
   int* rows = flags + (size_t)c.B * c.H_kv * n_flags;
   // The keys take turns of one a thread: 1024 threads where all CTAs are resident at once with
   // them (65536 slots of 4 heads: 31 us for the call, 35 with 512), else 512 (64 heads of 16384
-  // slots: 60 us, 72 with 1024, whose 512 CTAs came in two waves).
-  auto select = [&](auto kernel, int threads) {
+  // slots: 60 us, 72 with 1024, whose 512 CTAs came in two waves). Up to 2048 slots one CTA is
+  // no slower than eight (8 heads of 2048: 13 and 14 us), and up to 8192 it is faster where the
+  // eights come in several waves (300 heads of 1025 slots 21 and 68 us, of 8192 104 and 124; 64
+  // heads of 8192, in one wave, 40 and 32).
+  auto select = [&](auto kernel, int ctas, int threads, int most) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               select_run(kMaxBlocks * kBlock, threads) * (int)sizeof(uint32_t));
+                                               select_run(most, ctas, threads) * (int)sizeof(uint32_t));
     if (e != cudaSuccess) return e;
-    return launch_overlapped(kernel, dim3(c.B * c.H_kv * kSelCluster), threads,
-                             select_run(c.cap, threads) * sizeof(uint32_t), s, c, lens, (int)budget, (int)n_sink,
+    return launch_overlapped(kernel, dim3(c.B * c.H_kv * ctas), threads,
+                             select_run(c.cap, ctas, threads) * sizeof(uint32_t), s, c, lens, (int)budget, (int)n_sink,
                              (int)n_recent, kept, lens_out, dst_table, (int)(weight_out == c.weight), flags, n_flags, rows);
   };
-  cudaError_t e = c.B * c.H_kv * kSelCluster <= 2 * 148 ? select(evict_select_kernel<1024>, 1024)
-                                                        : select(evict_select_kernel<512>, 512);
+  const int most = kMaxBlocks * kBlock, heads = c.B * c.H_kv;
+  const bool alone = c.cap <= 2048 || (c.cap <= kSelAlone && heads * 8 > 4 * 148);
+  cudaError_t e = alone                  ? select(evict_select_kernel<1, 512>, 1, 512, kSelAlone)
+                  : heads * 8 <= 2 * 148 ? select(evict_select_kernel<8, 1024>, 8, 1024, most)
+                                         : select(evict_select_kernel<8, 512>, 8, 512, most);
   if (e != cudaSuccess) return SLA_ERR_CUDA;
   auto run = [&](auto kernel) {
     return launch_overlapped(kernel, dim3((unsigned)(c.B * c.H_kv * nd)), kCta, 0, s, c, (const int32_t*)kept, lens,

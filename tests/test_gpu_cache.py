@@ -619,6 +619,18 @@ def test_evict_keeps_the_heaviest(kind, d, budget, n_sink, n_recent, in_place):
 
 
 @pytest.mark.parametrize("in_place", [True, False])
+@pytest.mark.parametrize("B,max_blocks", [(5, 36), (75, 36), (5, 32), (5, 33)])
+def test_evict_few_and_many_heads(B, max_blocks, in_place):
+    """One CTA or a cluster selects, whatever the lengths are; many equal weights."""
+    p = Pair(B=B, H=1, H_kv=1, d=64, max_blocks=max_blocks, kind=INT8, spare=6 * B, seed=B + max_blocks)
+    p.fill([max_blocks * 64, 0, 1, 333, 334] + [(97 * i) % 1500 for i in range(B - 5)], std=2.0)
+    p.o.weight[:] = np.random.default_rng(B).integers(0, 30, p.o.weight.shape) / 8.0
+    p.c.weight.copy_(torch.from_numpy(p.o.weight))
+    dst, _ = run_evict(p, 333, 3, 70, in_place)
+    p.check(dst)
+
+
+@pytest.mark.parametrize("in_place", [True, False])
 def test_evict_odd_weights(in_place):
     p = Pair(B=1, H=1, H_kv=1, d=64, max_blocks=4, spare=8, seed=31)
     p.fill([250])
