@@ -587,11 +587,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 // ---------------------------------------------------------------------------
 // A CTA of `ctas` takes an equal run of the tiles, which are few: a CTA's warps wait for one
 // another's loads of scores (a slot's rows are a line), yet share the parts of their rows. A
-// warp a tile (list entries that name no block are passed over), a lane two slots. lse: this warp's place for the log2-sum-exp of the tile's rows, put together
-// from the parts of its segments (run: tiles of a part), or taken from a.lse where run is 0;
-// infinite for rows that add nothing. Bound by the chain of loads (8 sequences of up to 8191
-// tokens, 4 KV heads, 16 rows: 5 to 8 us beside the join): what can start before the rows'
-// sums does.
+// warp a tile (list entries that name no block are passed over), a lane two slots. lse: this
+// warp's place for the log2-sum-exp of the tile's rows, put together from the parts of its
+// segments (run: tiles of a part), or taken from a.lse where run is 0; infinite for rows that
+// add nothing. Bound by the chain of loads (8 sequences of up to 8191 tokens, 4 KV heads, 16
+// rows: 5 to 8 us beside the join): what can start before the rows' sums does.
 __device__ void weigh(const CacheView& c, const Step& a, const Lines& l, unsigned cta, unsigned ctas, unsigned warp,
                       unsigned warps, int lane, float* lse, unsigned run) {
   const unsigned per = c.H_kv, total = (unsigned)l.cum[c.B] * per;
