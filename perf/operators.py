@@ -161,13 +161,14 @@ def work(case):
 # ---------------------------------------------------------------------------
 
 def pow2_scale(amax, kind):
-    """The least power of two s >= 2^-110 with amax <= 448 s (e4m3) or 127 s (int8)."""
+    """The least power of two s with amax <= 448 s (e4m3) or 127 s (int8); 1 where amax is 0."""
     mant, e = torch.frexp(amax)
     if kind == E4M3:
         e = e - 9 + (mant > 0.875).int()
     else:
         e = e - 7 + (mant > 0.9921875).int()
-    return torch.ldexp(torch.ones_like(amax), torch.where(amax == 0, -110, e).clamp(-110, 120))
+    s = torch.ldexp(torch.ones_like(amax), e.clamp(-110, 120))
+    return torch.where(amax == 0, torch.ones_like(s), s)
 
 
 def to_codes(x, kind):
@@ -458,7 +459,7 @@ def _values64(codes, scale, kind):
 def _scale64(x, kind):
     a = float(x.abs().max()) if x.numel() else 0.0
     if a == 0:
-        return 2.0 ** -110
+        return 1.0
     top = 448.0 if kind == E4M3 else 127.0
     e = math.floor(math.log2(a / top)) - 1
     while top * 2.0 ** e < a:
