@@ -494,6 +494,11 @@ __device__ __forceinline__ int first_kept(const int32_t* from, int m, int slot) 
   return lo;
 }
 
+// Old scale / new scale 2^e, a finite number: beside an outlier that is evicted a row may have
+// codes of 0 only, and its page's scale times 2^110 can be beyond fp32, which would make them
+// NaN. Other codes never ask for more than 2^18: 2^-9 at least, they become 448 at most.
+__device__ __forceinline__ float scale_ratio(float old, int e) { return fminf(old * exp2_int(-e), 1048576.f); }
+
 template <int KIND, int D>
 __global__ void __launch_bounds__(kCta, 5) evict_move_kernel(const CacheView c, const int32_t* kept,
                                                           const int32_t* lens, int budget, const int32_t* dst_table,
@@ -599,8 +604,8 @@ __global__ void __launch_bounds__(kCta, 5) evict_move_kernel(const CacheView c, 
   for (int i = 0; i < NT; ++i) {
     const int task = tid + kCta * i, r = task / C, ch = task % C;
     const size_t at = (ph * kBlock + r) * D + ch * 16;
-    if (ks[i] != kt) kc[i] = recode16<KIND>(kc[i], ks[i] * exp2_int(-ke));
-    if (vs[i] != vt) vc[i] = recode16<KIND>(vc[i], vs[i] * exp2_int(-ve));
+    if (ks[i] != kt) kc[i] = recode16<KIND>(kc[i], scale_ratio(ks[i], ke));
+    if (vs[i] != vt) vc[i] = recode16<KIND>(vc[i], scale_ratio(vs[i], ve));
     *reinterpret_cast<uint4*>(c.k + at) = kc[i];
     *reinterpret_cast<uint4*>(c.v + at) = vc[i];
     if (full) *reinterpret_cast<uint4*>(tile + r * D + ch * 16) = kc[i];

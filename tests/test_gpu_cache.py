@@ -679,6 +679,54 @@ def test_evict_longest():
     p.check(dst)
 
 
+def fill_with_outliers(p, big):
+    """130 tokens whose first two blocks each hold one element `big` in every KV head, of keys and
+    of values: their other rows are rounded to 0. Returns the outliers' slots."""
+    k, v = p.kv(130)
+    for at, d in ((5, 3), (70, 40)):
+        k[:, :, at, d] = big
+        v[:, :, at, d + 1] = -big
+    p.append(k, v)
+    p.status((0, 0) if np.isfinite(big) else (sla.SLA_ERR_DEVICE_CHECK, 113))
+    assert not p.o.k[p.table[0, :2]][:, :, :5].any() and not p.o.v[p.table[0, :2]][:, :, :5].any()
+    return [5, 70]
+
+
+@pytest.mark.parametrize("in_place", [True, False])
+@pytest.mark.parametrize("kind", [E4M3, INT8])
+@pytest.mark.parametrize("big", [2.0 ** 30, float("inf")])
+@pytest.mark.parametrize("budget", [20, 64, 70])
+def test_evict_of_an_outlier_leaves_the_zeros_beside_it(kind, big, budget, in_place):
+    """New blocks of zero codes only, from pages of a large scale: the least scale, codes of 0."""
+    p = Pair(B=1, H=2, H_kv=2, d=64, max_blocks=3, kind=kind, seed=41)
+    gone = fill_with_outliers(p, big)
+    w = np.random.default_rng(budget).integers(1, 40, p.o.weight.shape).astype(np.float64)
+    w[:, :, gone] = w[:, :, 128:] = 0
+    p.o.weight[:] = w
+    p.c.weight.copy_(torch.from_numpy(w))
+    dst, kept = run_evict(p, budget, 0, 0, in_place)
+    assert not np.isin(kept, gone).any()
+    p.check(dst)
+
+
+@pytest.mark.parametrize("kind", [E4M3, INT8])
+def test_evict_joins_zeros_of_a_large_scale_and_tiny_numbers(kind):
+    """Zero codes of a page of scale 2^112 or so move into a block whose scale is the least one."""
+    p = Pair(B=1, H=1, H_kv=1, d=64, max_blocks=2, kind=kind, seed=42)
+    k, v = p.kv(128)
+    for x in (k, v):
+        x[:, :, 64:] = (x[:, :, 64:].float() * 2.0 ** -111).bfloat16()
+        x[:, :, 9, 1] = 2.0 ** 120
+    p.append(k, v)
+    p.status()
+    p.o.weight[:] = 1.0
+    p.o.weight[0, 0, 9] = 0
+    p.c.weight.copy_(torch.from_numpy(p.o.weight))
+    dst, kept = run_evict(p, 127, 0, 0, False)
+    assert 9 not in kept and p.o.k[dst[0, 0], 0, 63].any() and not p.o.k[dst[0, 0], 0, :63].any()
+    p.check(dst)
+
+
 def test_evict_in_a_captured_graph():
     """Replayed twice on the same cache, other weights each time, in place and packed again."""
     p = Pair(B=2, H=2, H_kv=2, d=64, max_blocks=10, kind=INT8, spare=0, seed=37)
