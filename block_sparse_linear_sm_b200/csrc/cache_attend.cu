@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
       const int ex = max((int)(__float_as_uint(top) >> 23) - 127, -100);
-      const float up = exp2_int(14 - ex);
+      const float up = row_factor(top, ex);
       if (q4 == 0) mi.qs[8 * warp + g] = exp2_int(ex - 14) * (c.scale * 1.4426950408889634f);
 #pragma unroll
       for (int s = 0; s < KS; ++s)

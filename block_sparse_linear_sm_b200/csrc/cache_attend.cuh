@@ -203,6 +203,11 @@ __device__ __forceinline__ void tma_load_rows(uint32_t dst, const CUtensorMap* m
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(0), "r"(row)
       : "memory");
 }
+// What a query row of largest magnitude `top`, exponent ex, is multiplied by for fp16. NaN where
+// it holds an infinity: the row's scores are to be NaN, and minus infinity means masked.
+__device__ __forceinline__ float row_factor(float top, int ex) {
+  return top < INFINITY ? exp2_int(14 - ex) : __int_as_float(0x7fffffff);
+}
 __device__ __forceinline__ float log2_sum(float m, float l) { return l == 0.f ? -INFINITY : m + log2f(l); }
 
 

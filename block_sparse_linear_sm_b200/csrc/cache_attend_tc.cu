@@ -452,7 +452,7 @@ __device__ bool rows_of_step(const CacheView& c, const Step& a, const Lines& l, 
           }
         }
         const int ex = max((int)(__float_as_uint(top) >> 23) - 127, -100);
-        const float up = exp2_int(14 - ex);
+        const float up = row_factor(top, ex);
         qs = exp2_int(ex - 14) * (c.scale * 1.4426950408889634f);
         const uint32_t at = smem_u32(smem + Sm::off_q) + r * 128;
 #pragma unroll

@@ -447,6 +447,34 @@ def test_attend_nan_query_adds_no_weight():
     assert abs(p.c.weight[0, 0].sum().item() - 3) < 3e-5 and abs(want[0, 0].sum().item() - 4) < 4e-5
 
 
+@pytest.mark.parametrize("H,T", [(4, 1), (5, 3), (68, 1), (30, 3)])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_attend_infinite_query_beside_keys_of_one_sign(H, T, sign):
+    """All its scores are +inf or all -inf; one key, some, many parts, none."""
+    p = Pair(B=4, H=H, H_kv=1, d=64, max_blocks=32, seed=24)
+    k, v = p.kv(2000)
+    k[..., 7] = k[..., 7].abs() + 0.5
+    p.append(k, v, [T, 100, 2000, 0])
+    p.c.weight.zero_()
+    n_new = [T, T, T, 0]
+    q = p.queries(T)
+    want = p.attend(q, n_new)
+    weight = p.c.weight.clone()
+    bad = q.clone()
+    for b in range(4):
+        bad[b, 1, T - 1, 7] = sign * float("inf")
+    p.c.weight.zero_()
+    out = p.attend(bad, n_new)
+    p.status()
+    assert torch.isnan(out[:3, 1, T - 1]).all() and not out[3].any()
+    rest = torch.ones(4, H, T, dtype=torch.bool)
+    rest[:, 1, T - 1] = False
+    assert torch.equal(out[rest], want[rest])
+    # the row's share is missing, and nothing else
+    lost = (weight - p.c.weight).sum(dim=(1, 2)).tolist()
+    assert all(abs(x - y) <= 2.0 ** -16 * H * T for x, y in zip(lost, (1, 1, 1, 0)))
+
+
 def test_attend_shared_pages():
     """Sequences may share pages that are only read."""
     p = Pair(B=3, H=4, H_kv=2, d=64, max_blocks=4, seed=15)
