@@ -16,7 +16,7 @@
 // half of what 16 do:
 //   S^T[64 slots x rows] = K Q^T; the scales of page, row and softmax in fp32;
 //   m' = max(m, colmax S^T), P = 2^(S - m' + 15) as fp16, l = l 2^(m - m') + 2^-15 sum P;
-//   O^T[d x rows] = O^T 2^(m - m') + 2^-15 v_scale * (V^T P^T).
+//   O^T[d x rows] = O^T 2^(m - m') + 2^-15 v_scale * (V^T P^T), held times 2^-18 (kOutShift).
 // The 15 keeps P's smallest terms out of fp16's subnormals: a weight of 2^-29 still has 11
 // bits. Q is scaled by a power of two a row so that its largest element is in [2^14, 2^15):
 // bf16 elements down to 2^-28 of it are then fp16 numbers exactly.
@@ -339,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       const Tile cur = ring.req;
       const int j0 = cur.block * kBlock;
       const bool chosen = cur.chosen;
-      const float ks = ring.req_ks, vs = ring.req_vs * exp2_int(-(int)kShift);
+      const float ks = ring.req_ks, vs = ring.req_vs * exp2_int(-(int)kShift - kOutShift);
       const uint32_t slot_k = ring.used % kSlots;
       if (!dead && !tc::mbar_wait(ring.bars + 8 * slot_k, (ring.used / kSlots) & 1, &mi.abort)) dead = true;
       const uint32_t kbase = ring.data + slot_k * Ring<D>::kPage;
@@ -565,7 +565,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         reinterpret_cast<float4*>(a.part_o)[part * (kRows * D / 4) + e] = y;
       } else if (row0 + r < a.rows) {
         const bool empty = all == 0.f || (row0 + r) % a.T >= n;
-        const float inv = 1.f / all;
+        const float inv = 1.f / out_divisor(all);
         *reinterpret_cast<uint2*>(a.out + (qrow0 + row0 + r) * D + 4 * d4) =
             empty ? make_uint2(0u, 0u) : make_uint2(pack_bf16(y.x * inv, y.y * inv), pack_bf16(y.z * inv, y.w * inv));
         if (d4 == 0 && a.lse != nullptr) a.lse[qrow0 + row0 + r] = log2_sum(top, all);
@@ -739,9 +739,10 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const CacheView c, c
   }
   if (!there) return;
   const bool valid = row % a.T < l.fresh[b] && sum != 0.f;
+  const float by = out_divisor(sum);
 #pragma unroll
   for (int e = 0; e < E; e += 2)
-    *reinterpret_cast<uint32_t*>(a.out + qrow * D + lane * E + e) = valid ? pack_bf16(o[e] / sum, o[e + 1] / sum) : 0u;
+    *reinterpret_cast<uint32_t*>(a.out + qrow * D + lane * E + e) = valid ? pack_bf16(o[e] / by, o[e + 1] / by) : 0u;
   if (lane == 0 && a.lse != nullptr) a.lse[qrow] = log2_sum(m, sum);
 }
 

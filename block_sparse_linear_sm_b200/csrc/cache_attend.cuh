@@ -12,12 +12,20 @@ namespace attend {
 // P is 2^(score - maximum + kShift) in fp16
 constexpr float kShift = 15.f;
 
+// The unnormalised output is held times 2^-kOutShift in fp32: values are up to 2^120, a sequence
+// has up to 2^18 tokens, and the kernel for many rows lets a weight be up to 2^7, so the sum is
+// below 2^128 with 2^-18 and would not be without. At the other end an addition is off by 2^-150
+// at most, which is 2^-132 of output, below bf16's least normal number by 2^6.
+constexpr int kOutShift = 18;
+// what such a sum is divided by: the row's sum of weights, l
+__device__ __forceinline__ float out_divisor(float l) { return l * exp2_int(-kOutShift); }
+
 struct Step {
   const __nv_bfloat16* q;
   const int32_t *lens, *n_new, *sel;
   __nv_bfloat16* out;
   float* part_ml;   // [slots][2][rows of a group]: m, l of a partial
-  float* part_o;    // [slots][rows of a group][D]
+  float* part_o;    // [slots][rows of a group][D], times 2^-kOutShift
   float* lse;       // [B, H, T] log2-sum-exp (with weights)
   float* scores;    // [tiles of all (sequence, KV head)][64][score_rows] (with weights)
   int T, top_n, window, rows, groups;  // rows = T * group of a KV head, in groups of group_rows

@@ -11,7 +11,8 @@
 //   warp 1          issues S = Q K^T (M 128, N 64) and, one page behind, P V (M 128, N d) with
 //                   P as the operand in TMEM;
 //   warps 4 - 7     own a row a thread: maximum, P = 2^(S - m + 8) as fp16 back to TMEM, and, a
-//                   page behind, O = O + 2^-8 v_scale * (P V) in fp32 registers.
+//                   page behind, O = O + 2^-8 v_scale * (P V) in fp32 registers (times 2^-18,
+//                   kOutShift).
 // Each page's P V goes to a buffer of its own (two, in turn) instead of accumulating in TMEM:
 // pages have value scales of their own, and with O in registers neither they nor a new maximum
 // need a pass over TMEM. m is raised, and O scaled, only when a maximum exceeds it by 2^7, so
@@ -406,7 +407,7 @@ __device__ bool rows_of_step(const CacheView& c, const Step& a, const Lines& l, 
         if (whole) {
           if (row < a.rows) {
             const bool empty = all == 0.f || pos < 0;
-            const float inv = 1.f / all;
+            const float inv = 1.f / out_divisor(all);
             uint4* out = reinterpret_cast<uint4*>(a.out + qrow * D);
 #pragma unroll
             for (int u = 0; u < D / 8; ++u) {
@@ -546,7 +547,7 @@ __device__ bool rows_of_step(const CacheView& c, const Step& a, const Lines& l, 
       for (int i = 0; i < D / 2; ++i) o[i] = tc::fmul2(o[i], a2);
     }
     owed = true;
-    owed_vs = x.vs * exp2_int(-(int)kTcShift);
+    owed_vs = x.vs * exp2_int(-(int)kTcShift - kOutShift);
     ++page;
   }
 }

@@ -530,6 +530,60 @@ def test_attend_longest_sequence(T, H):
     p.check_attend(p.queries(T), n_new=[T, min(T, 1)])
 
 
+@pytest.mark.parametrize("kind", [E4M3, INT8])
+@pytest.mark.parametrize("H,d", [(4, 64), (66, 64), (16, 128), (66, 128)])
+def test_attend_many_values_of_the_largest_magnitude(kind, H, d):
+    """320 tokens of +-2^120 at equal weights: their unnormalised sum is beyond fp32."""
+    p = Pair(B=2, H=H, H_kv=1, d=d, max_blocks=6, kind=kind, seed=25)
+    k, v = p.kv(320)
+    v[:] = 2.0 ** 120
+    v[..., ::2] = -(2.0 ** 120)
+    p.append(k, v, [320, 300])
+    q = p.queries(1) * 0
+    out = p.attend(q, weight=False)
+    p.status()
+    want, mag, _ = p.o.attend(f64(q), p.lens, [1, 1], None, 0)
+    assert np.all(np.abs(f64(out) - want) <= 2.0 ** -8 * np.abs(want) + (2.0 ** -11 + 2.0 ** -16) * mag)
+
+
+@pytest.mark.parametrize("H", [2, 16, 70])
+def test_attend_longest_sequence_of_the_largest_values(H):
+    """262144 tokens of 2^120; the first block of every 28 has scores 2^6.5 below the others, so
+    that a maximum taken from it stays behind for the whole run of a CTA."""
+    p = Pair(B=1, H=H, H_kv=1, d=64, max_blocks=4096, kind=INT8, seed=26, garbage=False)
+    p.table[0] = np.where(np.arange(4096) % 28 == 0, 0, 1)
+    p.o.table = p.table
+    p.c.block_table.copy_(i32(p.table))
+    for name in ("k", "v"):
+        codes = np.zeros(getattr(p.o, name)[:2].shape)
+        codes[:] = 64
+        if name == "k":
+            codes[0] = 0
+        getattr(p.o, name)[:2] = codes
+        getattr(p.c, name)[:2] = torch.from_numpy(codes.astype(np.int8)).cuda()
+    p.o.ks[:], p.o.vs[:] = 2.0 ** -6, 2.0 ** 114
+    p.c.k_scale.fill_(2.0 ** -6), p.c.v_scale.fill_(2.0 ** 114)
+    p.lens = np.array([LONGEST])
+    # q . k * scale = 64 * 4.5 / 8 * 1 / 8 = 4.5: e^4.5 is 2^6.5, and the others' k is 0
+    q = bf16(np.full((1, H, 1, 64), 4.5 / 8))
+    out = p.attend(q, weight=False)
+    p.status()
+    assert np.all(np.abs(f64(out) - 2.0 ** 120) <= (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -16) * 2.0 ** 120)
+
+
+@pytest.mark.parametrize("H", [4, 66])
+def test_attend_values_of_the_least_scale(H):
+    """Pages at the least scale: the output is as good as that of other pages."""
+    p = Pair(B=1, H=H, H_kv=1, d=64, max_blocks=6, kind=INT8, seed=27)
+    k, v = p.kv(330)
+    p.append(k, (v.float() * 2.0 ** -106).bfloat16())
+    assert (p.o.vs[p.table] == 2.0 ** -110).all()
+    q = p.queries(1)
+    out = p.attend(q, weight=False)
+    want, mag, _ = p.o.attend(f64(q), p.lens, [1], None, 0)
+    assert np.all(np.abs(f64(out) - want) <= 2.0 ** -8 * np.abs(want) + (2.0 ** -11 + 2.0 ** -16) * mag)
+
+
 @pytest.mark.parametrize("T", [2, 9])
 def test_attend_writes_the_same_bits_again(T):
     p = Pair(B=4, H=16, H_kv=2, d=128, max_blocks=40, seed=18)
