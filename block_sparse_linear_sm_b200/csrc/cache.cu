@@ -52,6 +52,7 @@ sla_status check_cache(const sla_cache_config* c, const sla_cache* m, CacheView*
   view->cap = c->max_blocks * kBlock;
   view->kind = c->kind;
   view->scale = c->scale > 0.f ? c->scale : 1.f / sqrtf((float)c->d);
+  view->scale64 = c->scale > 0.f ? (double)c->scale : 1.0 / sqrt((double)c->d);
   return SLA_OK;
 }
 

@@ -23,6 +23,7 @@ struct CacheView {
   int* status;
   int B, H, H_kv, group, d, n_pages, max_blocks, cap, kind;
   float scale;
+  double scale64;  // the router's: 1 / sqrt(128) rounded to fp32 is off by 1.7e-8 of it
 };
 
 // Every kernel of the cache is launched so that it may start while the one before it in the

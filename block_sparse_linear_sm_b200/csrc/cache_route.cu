@@ -158,7 +158,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 4)
           for (int i = 0; i < 2; ++i)
             if (8 * i < heads)
               score[(8 * i + (lane >> 2)) * pitch + u + at] =
-                  there ? (acc[i][0][e] + acc[i][1][e]) * (double)c.scale : -INFINITY;
+                  there ? (acc[i][0][e] + acc[i][1][e]) * c.scale64 : -INFINITY;
         }
       }
     }

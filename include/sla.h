@@ -490,7 +490,8 @@ SLA_API sla_status sla_cache_append(const void* k, const void* v, const sla_cach
  * block): qbar_h = mean of head h's valid query rows; over the past blocks j <
  * (lens[b] - n_new[b]) / 64, P_h = softmax_j(qbar_h . k_mean_j * scale); the top_n blocks
  * of largest sum of P_h over the group's heads, equal sums by lower index. Computed in
- * fp64, like sla_route.
+ * fp64, like sla_route, but with 1/sqrt(128) in fp64 too (scale 0, d 128), which sla_route
+ * rounds to fp32: blocks whose sums agree to 1e-7 or so may change places between the two.
  *   q      bf16 [B, H, T, d], 1 <= T <= 64, rows at n_new[b] and beyond not read
  *   lens   int32 [B]: cached tokens, the step's own included (as after sla_cache_append)
  *   n_new  int32 [B] or NULL (T): valid query rows, the last n_new[b] cached tokens

@@ -645,6 +645,44 @@ def test_route_equal_blocks_by_lower_index():
     assert run_route(p, q, 3).tolist() == [[[0, 1, 11]]]
 
 
+def test_route_scale_is_not_rounded():
+    """1 / sqrt(128) rounded to fp32 is off by 1.7e-8 of it, which would change the order of two
+    blocks whose sums are closer than that. The heads' scores are (x, 0, 9) and (0, 1, 0): where
+    x = 8.45 or so, blocks 0 and 1 have equal sums. x is put halfway between the places where the
+    two scales find them equal."""
+    p = Pair(B=1, H=2, H_kv=1, d=128, max_blocks=4, seed=28, garbage=False)
+    exact, rounded = 1 / np.sqrt(128.0), float(np.float32(1) / np.sqrt(np.float32(128)))
+    q = np.zeros((1, 2, 1, 128))
+    q[0, 0, 0, 0], q[0, 1, 0, 1], q[0, 0, 0, 2] = 8.0, 8.0, 2.0 ** -10
+    mean = np.zeros((4, 128), np.float32)
+    mean[2, 0], mean[1, 1] = 9 / (8 * exact), 1 / (8 * exact)
+
+    def ahead(at, x, scale):
+        """Sum of block 0 less that of block 1 with mean[0, at] = x."""
+        m = mean[:3].astype(np.float64)
+        m[0, at] = x
+        e = [np.exp(m @ q[0, h, 0] * scale) for h in range(2)]
+        return sum((t[0] - t[1]) / t.sum() for t in e)
+
+    def equal(at, scale, lo, hi):
+        assert ahead(at, lo, scale) < 0 < ahead(at, hi, scale)
+        for _ in range(100):
+            mid = (lo + hi) / 2
+            lo, hi = (mid, hi) if ahead(at, mid, scale) < 0 else (lo, mid)
+        return lo
+
+    mean[0, 0] = equal(0, exact, 0.0, 20.0)
+    mean[0, 2] = (equal(2, exact, -1.0, 1.0) + equal(2, rounded, -1.0, 1.0)) / 2
+    x = float(mean[0, 2])
+    assert (ahead(2, x, exact) < 0) != (ahead(2, x, rounded) < 0)
+    p.lens = np.array([3 * 64 + 1])
+    p.c.k_mean[torch.from_numpy(p.table[0]).cuda(), 0] = torch.from_numpy(mean).cuda()
+    p.o.mean = f64(p.c.k_mean)
+    want, gap = p.o.route(q, p.lens, [1], 2)
+    assert gap > 1e-9
+    np.testing.assert_array_equal(run_route(p, bf16(q), 2), want)
+
+
 def test_route_leaves_out_bad_pages():
     p = Pair(B=1, H=2, H_kv=1, d=64, max_blocks=6, seed=23)
     p.fill([6 * 64])
