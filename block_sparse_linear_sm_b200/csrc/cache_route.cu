@@ -130,7 +130,11 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 4)
           }
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] *= inv_n;
+        for (int e = 0; e < 8; ++e) {
+          x[e] *= inv_n;
+          // every score of the head is to be NaN then, not one infinity beside means of one sign
+          if (isinf(x[e])) x[e] = __longlong_as_double(0x7ff8000000000000ll);
+        }
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) qbar[h >> 3][(d + e) % S][4 * (h & 7) + (d + e) / S] = x[e];

@@ -497,7 +497,7 @@ SLA_API sla_status sla_cache_append(const void* k, const void* v, const sla_cach
  *   n_new  int32 [B] or NULL (T): valid query rows, the last n_new[b] cached tokens
  *   sel    int32 [B, H_kv, top_n], 1 <= top_n <= 64: ascending, -1 behind the last
  * A past block whose page number is out of range scores -inf and is never picked; where a
- * query or mean holds a NaN nothing is.
+ * query row or a mean holds a NaN or a query row an infinity nothing is.
  */
 SLA_API sla_status sla_cache_route(const void* q, const sla_cache_config* cfg, const sla_cache* cache,
                                    int32_t T, const int32_t* lens, const int32_t* n_new,

@@ -683,6 +683,22 @@ def test_route_scale_is_not_rounded():
     np.testing.assert_array_equal(run_route(p, bf16(q), 2), want)
 
 
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+def test_route_picks_nothing_for_a_query_that_is_not_finite(value):
+    """Beside means of one sign an infinity makes every score the same infinity."""
+    p = Pair(B=2, H=6, H_kv=2, d=64, max_blocks=10, seed=29)
+    k, v = p.kv(600)
+    k[..., 7] = k[..., 7].abs() + 0.5
+    p.append(k, v, [600, 70])
+    q = p.queries(2)
+    want, gap = p.o.route(f64(q), p.lens, [2, 2], 3)
+    assert gap > 1e-9
+    q[:, 4, 1, 7] = value           # a head of the second group
+    want[:, 1] = -1
+    np.testing.assert_array_equal(run_route(p, q, 3), want)
+    p.status()
+
+
 def test_route_leaves_out_bad_pages():
     p = Pair(B=1, H=2, H_kv=1, d=64, max_blocks=6, seed=23)
     p.fill([6 * 64])
