@@ -4,6 +4,8 @@
 // page of one head is one contiguous run of 64 * d bytes.
 #include <math.h>
 
+#include <algorithm>
+
 #include "cache.cuh"
 #include "tc.cuh"
 
@@ -639,8 +641,10 @@ sla_status sla_cache_append(const void* k, const void* v, const sla_cache_config
   if (!aligned_to(k, 16) || !aligned_to(v, 16) || !aligned_to(lens, 4) || !aligned_to(n_new, 4) ||
       !aligned_to(lens_out, 4))
     return SLA_ERR_INVALID_ARG;
-  if (T > c.cap) return SLA_ERR_INVALID_ARG;  // no sequence could take them
-  const int touched = (T + kBlock - 2) / kBlock + 1;  // blocks that T tokens can reach into
+  if (T > c.cap && !n_new) return SLA_ERR_INVALID_ARG;  // no sequence could take them
+  // blocks that the tokens one sequence takes can reach into
+  const int most = T < c.cap ? T : c.cap;
+  const int touched = std::min((most + kBlock - 2) / kBlock + 1, c.max_blocks);
   const dim3 grid((unsigned)(touched * c.H_kv), (unsigned)c.B, 2);
   cudaStream_t s = (cudaStream_t)stream;
   auto run = [&](auto kernel) {

@@ -466,7 +466,8 @@ SLA_API sla_status sla_cache_validate_config(const sla_cache_config* cfg);
 /*
  * Writes the first n_new[b] of T new tokens of each sequence into slots lens[b] ..
  * lens[b] + n_new[b] - 1.
- *   k, v      bf16 [B, H_kv, T, d], T >= 1; rows at n_new[b] and beyond are not read
+ *   k, v      bf16 [B, H_kv, T, d], T >= 1 (at most 64 * max_blocks where n_new is NULL); rows
+ *             at n_new[b] and beyond are not read
  *   lens      int32 [B]: cached tokens before the call, 0 .. 64 * max_blocks
  *   n_new     int32 [B], 0 .. T; NULL: T for every sequence
  *   lens_out  int32 [B] or NULL: receives lens[b] + n_new[b]; not lens itself

@@ -145,6 +145,15 @@ def test_evict_refusals():
     assert sla.sla_cache_evict_workspace_bytes(cfg, 0) == sla.sla_cache_evict_workspace_bytes(cfg, 513) == 0
 
 
+def test_a_buffer_longer_than_a_sequence_needs_its_lengths():
+    """Without n_new all T rows would be taken, which no sequence can hold."""
+    L, c = sla.lib(), ref(config())
+    for T in (8 * 64 + 1, 2**31 - 1):
+        assert L.sla_cache_append(16, 16, c, buffers(), T, 16, None, None, None) == IA
+    # with it only what the device sees can be wrong; refused here for its lens_out
+    assert L.sla_cache_append(16, 16, c, buffers(), 8 * 64 + 1, 1024, 2048, 1024, None) == IA
+
+
 def test_python_cache_refuses_tensors_that_the_kernels_could_not_take():
     with pytest.raises(ValueError, match="CUDA"):
         sla.SlaCache.empty(config(), device="cpu")

@@ -219,6 +219,24 @@ def test_append_reports_values_it_cannot_hold():
     p.status()
 
 
+@pytest.mark.parametrize("kind", [E4M3, INT8])
+def test_append_of_few_rows_from_a_buffer_longer_than_a_sequence(kind):
+    """T is the buffers' row pitch: n_new says what is taken."""
+    p = Pair(B=3, H=2, H_kv=2, d=64, max_blocks=2, kind=kind, seed=5)
+    for n_new in ([10, 0, 128], [100, 64, 0], [18, 1, 0]):
+        k, v = p.kv(300)
+        for b, n in enumerate(n_new):
+            k[b, :, n:] = v[b, :, n:] = float("nan")
+        p.append(k, v, n_new)
+        p.check()
+        p.status()
+    out = torch.zeros(3, dtype=torch.int32, device="cuda")
+    sla.sla_cache_append(k, v, p.cfg, p.c, i32(p.lens), i32([1, 300, 129]), out)
+    assert out.tolist() == p.lens.tolist()
+    p.status((sla.SLA_ERR_DEVICE_CHECK, 111))
+    p.check()
+
+
 def test_append_refuses_on_the_device_what_does_not_fit():
     p = Pair(B=5, H=1, H_kv=1, d=64, max_blocks=2)
     p.fill([10, 10, 10, 10, 10])
