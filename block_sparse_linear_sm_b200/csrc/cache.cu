@@ -13,6 +13,12 @@ namespace sla {
 
 static bool aligned_to(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
+// Whether two arrays of B lengths share memory: lengths are written while other blocks read.
+static bool lengths_overlap(const int32_t* a, const int32_t* b, int B) {
+  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b, n = (uintptr_t)B * sizeof(int32_t);
+  return a && b && x < y + n && y < x + n;
+}
+
 static sla_status check_sizes(const sla_cache_config* c) {
   if (c == nullptr) return SLA_ERR_INVALID_ARG;
   if (c->B < 1 || c->H < 1 || c->H_kv < 1 || c->d < 1 || c->n_pages < 1 || c->max_blocks < 1)
@@ -637,7 +643,8 @@ sla_status sla_cache_append(const void* k, const void* v, const sla_cache_config
   CacheView c;
   const sla_status st = check_cache(cfg, cache, &c);
   if (st != SLA_OK) return st;
-  if (!k || !v || !lens || T < 1 || lens == lens_out) return SLA_ERR_INVALID_ARG;
+  if (!k || !v || !lens || T < 1) return SLA_ERR_INVALID_ARG;
+  if (lengths_overlap(lens_out, lens, c.B) || lengths_overlap(lens_out, n_new, c.B)) return SLA_ERR_INVALID_ARG;
   if (!aligned_to(k, 16) || !aligned_to(v, 16) || !aligned_to(lens, 4) || !aligned_to(n_new, 4) ||
       !aligned_to(lens_out, 4))
     return SLA_ERR_INVALID_ARG;
@@ -671,7 +678,7 @@ sla_status sla_cache_evict(const sla_cache_config* cfg, const sla_cache* cache, 
   CacheView c;
   const sla_status st = check_cache(cfg, cache, &c);
   if (st != SLA_OK) return st;
-  if (!lens || !dst_table || !weight_out || !kept || !lens_out || !c.weight || lens == lens_out)
+  if (!lens || !dst_table || !weight_out || !kept || !lens_out || !c.weight || lengths_overlap(lens_out, lens, c.B))
     return SLA_ERR_INVALID_ARG;
   if (!aligned_to(lens, 4) || !aligned_to(dst_table, 4) || !aligned_to(weight_out, 16) || !aligned_to(kept, 4) ||
       !aligned_to(lens_out, 4))

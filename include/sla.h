@@ -470,7 +470,7 @@ SLA_API sla_status sla_cache_validate_config(const sla_cache_config* cfg);
  *             at n_new[b] and beyond are not read
  *   lens      int32 [B]: cached tokens before the call, 0 .. 64 * max_blocks
  *   n_new     int32 [B], 0 .. T; NULL: T for every sequence
- *   lens_out  int32 [B] or NULL: receives lens[b] + n_new[b]; not lens itself
+ *   lens_out  int32 [B] or NULL: receives lens[b] + n_new[b]; apart from lens and n_new
  * For each block written and KV head, K and V apart: with a the largest magnitude of the
  * block's new elements, a block whose first slot is written now gets scale pow2(a); an
  * open one gets scale max(old, pow2(a)), and where that is larger the codes it holds are
@@ -550,7 +550,8 @@ SLA_API sla_status sla_cache_attend(const void* q, const sla_cache_config* cfg, 
  *   weight_out  fp32 [B, H_kv, 64 * max_blocks]: the kept slots' weights at their new
  *               places, other places left alone; may be cache->weight
  *   kept        int32 [B, H_kv, budget]: the slot each kept token had, -1 behind the last
- *   lens_out    int32 [B]: min(lens[b], budget); not lens itself
+ *   lens_out    int32 [B]: min(lens[b], budget), 0 where lens[b] is out of range; apart from
+ *               lens
  * A sequence of at most budget tokens moves unchanged to its dst_table pages. Full new
  * blocks get their k_mean (when kept). budget > 64 * max_blocks: SLA_ERR_INVALID_ARG.
  * ws: sla_cache_evict_workspace_bytes bytes, 256-byte aligned, needs no initialisation.

@@ -145,6 +145,20 @@ def test_evict_refusals():
     assert sla.sla_cache_evict_workspace_bytes(cfg, 0) == sla.sla_cache_evict_workspace_bytes(cfg, 513) == 0
 
 
+@pytest.mark.parametrize("n_new", [None, 2048])
+def test_append_refuses_to_write_lengths_that_it_reads(n_new):
+    """lens_out may share no element (here two of four bytes) with lens or n_new."""
+    L, c = sla.lib(), ref(config())
+    for at in [1020, 1024, 1028] + ([2044, 2048, 2052] if n_new else []):
+        assert L.sla_cache_append(16, 16, c, buffers(), 1, 1024, n_new, at, None) == IA, at
+
+
+def test_evict_refuses_to_write_lengths_that_it_reads():
+    L, c = sla.lib(), ref(config())
+    for at in (1020, 1024, 1028):
+        assert L.sla_cache_evict(c, buffers(), 1024, 64, 0, 0, 16, 16, 16, at, 256, 1 << 20, None) == IA, at
+
+
 def test_a_buffer_longer_than_a_sequence_needs_its_lengths():
     """Without n_new all T rows would be taken, which no sequence can hold."""
     L, c = sla.lib(), ref(config())
