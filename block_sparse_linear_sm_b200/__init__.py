@@ -400,7 +400,8 @@ def _typed(x, name: str, shape, dtypes, index: int):
 
 class SlaCache:
     """The buffers of a paged 8-bit cache (sla_cache in include/sla.h). The tensors may be
-    changed in place but not replaced: the addresses are taken once.
+    changed in place but not replaced (the attributes are read-only): the addresses are taken
+    once.
 
     k, v          1-byte dtype [n_pages, H_kv, 64, d]
     k_scale, v_scale  float32 [n_pages, H_kv]
@@ -433,15 +434,21 @@ class SlaCache:
         c.weight = _typed(weight, "weight", (B, H_kv, 64 * max_blocks), f32, dev)
         c.block_table = _typed(block_table, "block_table", (B, max_blocks), i32, dev)
         c.status = _typed(status, "status", (64,), i32, dev)
-        self.k, self.v, self.k_scale, self.v_scale, self.k_mean = k, v, k_scale, v_scale, k_mean
-        self.weight, self.block_table, self.status = weight, block_table, status
-        self.device, self._c = k.device, c
-        self.index = dev
-        # the element type where the dtype names one (uint8 holds either)
-        self.kind = {torch.int8: SLA_CACHE_INT8, torch.float8_e4m3fn: SLA_CACHE_E4M3}.get(k.dtype)
         if v.dtype != k.dtype:
             raise ValueError("k and v must have the same dtype")
-        self.shape = (B, H_kv, d, n_pages, max_blocks)
+        # the element type where the dtype names one (uint8 holds either)
+        kind = {torch.int8: SLA_CACHE_INT8, torch.float8_e4m3fn: SLA_CACHE_E4M3}.get(k.dtype)
+        for name, x in dict(k=k, v=v, k_scale=k_scale, v_scale=v_scale, k_mean=k_mean, weight=weight,
+                            block_table=block_table, status=status, device=k.device, index=dev, kind=kind,
+                            shape=(B, H_kv, d, n_pages, max_blocks), _c=c).items():
+            object.__setattr__(self, name, x)
+
+    def __setattr__(self, name, value):
+        raise AttributeError(f"a cache's {name} cannot be replaced: its address is taken once; "
+                             f"write into the tensor, or build another SlaCache")
+
+    def __delattr__(self, name):
+        raise AttributeError(f"a cache's {name} cannot be replaced: its address is taken once")
 
     @classmethod
     def empty(cls, c, device="cuda", weight: bool = True, k_mean: bool = True) -> "SlaCache":

@@ -168,6 +168,17 @@ def test_a_buffer_longer_than_a_sequence_needs_its_lengths():
     assert L.sla_cache_append(16, 16, c, buffers(), 8 * 64 + 1, 1024, 2048, 1024, None) == IA
 
 
+def test_the_caches_tensors_cannot_be_replaced():
+    """Their addresses are taken once: another tensor in their place would never be read, and
+    the one that the kernels read would be gone."""
+    cache = object.__new__(sla.SlaCache)
+    for name in sla.SlaCache.__slots__:
+        with pytest.raises(AttributeError, match="replaced"):
+            setattr(cache, name, 1)
+        with pytest.raises(AttributeError, match="replaced"):
+            delattr(cache, name)
+
+
 def test_python_cache_refuses_tensors_that_the_kernels_could_not_take():
     with pytest.raises(ValueError, match="CUDA"):
         sla.SlaCache.empty(config(), device="cpu")
