@@ -213,8 +213,9 @@ __device__ bool produce(const CacheView& c, const Step& a, const Lines& l, Misc&
 // ---------------------------------------------------------------------------
 // warp 1: products
 // ---------------------------------------------------------------------------
+// *pages: pages whose S was issued; *outputs: those whose P V was.
 template <int D>
-__device__ bool multiply(Misc& mi, char* smem, uint32_t tmem, int lane) {
+__device__ bool multiply(Misc& mi, char* smem, uint32_t tmem, int lane, unsigned* pages, unsigned* outputs) {
   using Sm = Smem<D>;
   constexpr uint32_t kIdS = idesc_f16(128, 64, false), kIdO = idesc_f16(128, D, true);
   const uint64_t dq = tc::sw128_desc(smem_u32(smem + Sm::off_q), 16, 1024);
@@ -238,6 +239,7 @@ __device__ bool multiply(Misc& mi, char* smem, uint32_t tmem, int lane) {
       tc::mma_commit(smem_u32(&mi.v_empty[b]));
     }
     __syncwarp();
+    *outputs = i + 1;
     return true;
   };
   for (unsigned e = 0;; ++e) {
@@ -266,15 +268,12 @@ __device__ bool multiply(Misc& mi, char* smem, uint32_t tmem, int lane) {
       tc::mma_commit(smem_u32(&mi.k_empty[b]));
     }
     __syncwarp();
+    *pages = page + 1;
     if (owed && !values(page - 1)) return false;
     owed = true;
     ++page;
   }
-  if (owed && !values(page - 1)) return false;
-  // every commit has arrived before the block ends
-  for (unsigned i = page >= 2 ? page - 2 : 0; i < page; ++i)
-    if (!wait_all(&mi.k_empty[i & 1], i >> 1, mi) || !wait_all(&mi.v_empty[i & 1], i >> 1, mi)) return false;
-  return true;
+  return !owed || values(page - 1);
 }
 
 // ---------------------------------------------------------------------------
@@ -613,11 +612,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (unsigned i = issued > kRaw ? issued - kRaw : 0; i < issued; ++i)
         tc::mbar_wait(smem_u32(&mi.raw_full[i % kRaw]), (i / kRaw) & 1, &mi.never);
     } else if (warp == 1) {
-      ok = multiply<D>(mi, smem, tmem, lane);
+      unsigned pages = 0, outputs = 0;
+      ok = multiply<D>(mi, smem, tmem, lane, &pages, &outputs);
+      if (!ok) mi.abort = 1;
+      // products on their way end before TMEM and the block's memory are given back, also where
+      // another wait ran out
+      for (unsigned i = pages > 2 ? pages - 2 : 0; i < pages; ++i)
+        ok = tc::mbar_wait(smem_u32(&mi.k_empty[i & 1]), (i >> 1) & 1, &mi.never) && ok;
+      for (unsigned i = outputs > 2 ? outputs - 2 : 0; i < outputs; ++i)
+        ok = tc::mbar_wait(smem_u32(&mi.v_empty[i & 1]), (i >> 1) & 1, &mi.never) && ok;
+      ok = __all_sync(0xffffffffu, ok);
     }
   } else if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 240;");
     ok = rows_of_step<D>(c, a, l, mi, smem, tmem, lo, hi, warp, lane);
+    if (!ok) tc::tmem_st_wait();  // P, which was not handed over
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
     ok = convert<KIND, D>(mi, smem, tid & 127, lane);
