@@ -182,6 +182,17 @@ __device__ __forceinline__ void request_keys(Ring<D>& r, const CacheView& c, con
   }
 }
 
+// Waits for the ring's oldest page as a warp. Where the wait runs out the ring requests nothing
+// more: a barrier whose copy has not landed takes no second one, and the run ends.
+template <int D>
+__device__ __forceinline__ bool wait_page(Ring<D>& r, volatile int* abort) {
+  const uint32_t slot = r.used % kSlots;
+  if (__all_sync(0xffffffffu, tc::mbar_wait(r.bars + 8 * slot, (r.used / kSlots) & 1, abort))) return true;
+  r.next = r.end;
+  r.has_ahead = r.has_req = false;
+  return false;
+}
+
 // ---------------------------------------------------------------------------
 // the attention kernel
 // ---------------------------------------------------------------------------
@@ -340,9 +351,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       const int j0 = cur.block * kBlock;
       const bool chosen = cur.chosen;
       const float ks = ring.req_ks, vs = ring.req_vs * exp2_int(-(int)kShift - kOutShift);
-      const uint32_t slot_k = ring.used % kSlots;
-      if (!dead && !tc::mbar_wait(ring.bars + 8 * slot_k, (ring.used / kSlots) & 1, &mi.abort)) dead = true;
-      const uint32_t kbase = ring.data + slot_k * Ring<D>::kPage;
+      const uint32_t kbase = ring.data + ring.used % kSlots * Ring<D>::kPage;
+      if (!wait_page(ring, &mi.abort)) {
+        dead = true;
+        break;
+      }
 
       // scores: row g (+ 8) of tile t is slot 16 t + 4 (g / 2) + g % 2 (+ 2)
       float s[4][NR][4];
@@ -458,9 +471,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       }
 
       const uint64_t vs2 = tc::f2_pack(vs, vs);
-      const uint32_t slot_v = ring.used % kSlots;
-      if (!dead && !tc::mbar_wait(ring.bars + 8 * slot_v, (ring.used / kSlots) & 1, &mi.abort)) dead = true;
-      const uint32_t vbase = ring.data + slot_v * Ring<D>::kPage;
+      const uint32_t vbase = ring.data + ring.used % kSlots * Ring<D>::kPage;
+      if (!wait_page(ring, &mi.abort)) {
+        dead = true;
+        break;
+      }
       if (j0 + kBlock > L) {  // codes of slots behind the last token are whatever they are: they count as 0
         for (int e = (L - j0) * (D / 16) + lane; e < kBlock * (D / 16); e += 32) sts128(vbase + e * 16, 0u);
         __syncwarp();
