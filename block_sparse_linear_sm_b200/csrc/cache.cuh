@@ -139,24 +139,19 @@ __device__ __forceinline__ float max_magnitude16(const uint4& c) {
 // ---------------------------------------------------------------------------
 // checked device-side arguments
 // ---------------------------------------------------------------------------
-// cached tokens of sequence b, 0 where the value is out of range (*bad set)
+// n, or 0 where it is not in 0 .. most (*bad set)
+__device__ __forceinline__ int in_range(int n, int most, bool* bad) {
+  if (n >= 0 && n <= most) return n;
+  *bad = true;
+  return 0;
+}
+// cached tokens of sequence b
 __device__ __forceinline__ int checked_len(const int32_t* lens, int b, int cap, bool* bad) {
-  const int n = lens[b];
-  if (n < 0 || n > cap) {
-    *bad = true;
-    return 0;
-  }
-  return n;
+  return in_range(lens[b], cap, bad);
 }
 // valid query rows of sequence b
 __device__ __forceinline__ int checked_new(const int32_t* n_new, int b, int T, bool* bad) {
-  if (n_new == nullptr) return T;
-  const int n = n_new[b];
-  if (n < 0 || n > T) {
-    *bad = true;
-    return 0;
-  }
-  return n;
+  return n_new == nullptr ? T : in_range(n_new[b], T, bad);
 }
 // page of block j of sequence b, -1 (and reported) where the table's number is out of range
 __device__ __forceinline__ int checked_page(const CacheView& c, int b, int j) {

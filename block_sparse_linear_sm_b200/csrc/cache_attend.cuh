@@ -56,7 +56,9 @@ struct Lines {  // in shared memory
 };
 __host__ __device__ inline size_t lines_bytes(int B) { return align_up((size_t)(2 * B + 1) * 4 + B, 16); }
 
-// All threads of the block; ends with a barrier.
+// All threads of the block; ends with a barrier. The lengths are read from L2: join_kernel and
+// weight_kernel look at them before they wait (what wrote them was complete when the attention
+// kernel let them start), and a line in L1 may be older.
 static __device__ void scan_lines(const CacheView& c, const Step& a, char* smem, Lines* out, int* warp_sums) {
   Lines l;
   l.cum = reinterpret_cast<int*>(smem);
@@ -67,7 +69,8 @@ static __device__ void scan_lines(const CacheView& c, const Step& a, char* smem,
   int mine = 0;
   for (int b = b0; b < min(c.B, b0 + per); ++b) {
     bool bad = false;
-    const int L = checked_len(a.lens, b, c.cap, &bad), n = checked_new(a.n_new, b, a.T, &bad);
+    const int L = in_range(__ldcg(a.lens + b), c.cap, &bad);
+    const int n = a.n_new == nullptr ? a.T : in_range(__ldcg(a.n_new + b), a.T, &bad);
     if (bad && blockIdx.x == 0) report(c.status, SLA_ERR_DEVICE_CHECK, kDetailCacheLen);
     l.len[b] = L;
     l.fresh[b] = (uint8_t)n;

@@ -1040,6 +1040,40 @@ def test_streams_and_captured_steps():
     p.status()
 
 
+@pytest.mark.parametrize("B", [3, 24])
+def test_lengths_in_two_buffers_in_turn(B):
+    """Steps one behind the other without a copy or a wait between them, the lengths in one of two
+    buffers and then the other: every kernel of a step sees its own lengths."""
+    p = Pair(B=B, H=16, H_kv=2, d=64, max_blocks=20, kind=INT8, seed=62)
+
+    def kv(T):
+        """Every token has the same largest element, so that codes are never rounded again."""
+        k, v = (x.clamp(-3.5, 3.5) for x in p.kv(T))
+        k[..., 3], v[..., 5] = 4.0, -4.0
+        return k, v
+
+    steps = 60
+    p.append(*kv(1000), n_new=[(331 * b + 1) % 1001 for b in range(B)])
+    news, qs = [kv(1) for _ in range(steps)], [p.queries(1) for _ in range(steps)]
+    outs = [torch.empty_like(q) for q in qs]
+    lens = [i32(p.lens), torch.zeros(B, dtype=torch.int32, device="cuda")]
+    ws = torch.empty(sla.sla_cache_attend_workspace_bytes(p.cfg, 1, 0, 0, True), dtype=torch.uint8, device="cuda")
+    p.c.weight.zero_()
+    torch.cuda.synchronize()
+    for i, ((k, v), q, out) in enumerate(zip(news, qs, outs)):
+        old, new = lens[i % 2], lens[1 - i % 2]
+        sla.sla_cache_append(k, v, p.cfg, p.c, old, None, new)
+        sla.sla_cache_attend(q, p.cfg, p.c, new, None, None, 0, out, ws)
+    p.status()
+    # every row gave out a weight of 1 a step (rows of sums of 2^-16 relative error)
+    got = p.c.weight.sum(dim=2)
+    assert bool(((got - 8 * steps).abs() <= 8 * steps * 2.0 ** -16).all())
+    first = p.lens.copy()
+    for i, (q, out) in enumerate(zip(qs, outs)):
+        p.lens = first + i + 1
+        assert torch.equal(p.attend(q, weight=False), out), i
+
+
 def test_captured_beside_copies_and_a_second_stream():
     """Copies before, between and behind the calls, and the routing on a stream of its own that
     the attention waits for: each call sees what was written before it, replay after replay."""
