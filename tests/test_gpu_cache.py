@@ -881,6 +881,30 @@ def test_evict_joins_zeros_of_a_large_scale_and_tiny_numbers(kind):
     p.check(dst)
 
 
+@pytest.mark.parametrize("same_weights", [True, False])
+@pytest.mark.parametrize("own", [[0, 2], [1, 3], [3], [0, 1, 2]])
+def test_evict_some_blocks_in_place(own, same_weights):
+    """Blocks packed where they are beside blocks that move to new pages; weights in place or not."""
+    p = Pair(B=2, H=3, H_kv=3, d=64, max_blocks=12, kind=INT8, spare=8, seed=43)
+    p.fill([768, 500])
+    p.o.weight[:] = np.random.default_rng(len(own)).integers(0, 40, p.o.weight.shape) / 8.0
+    p.c.weight.copy_(torch.from_numpy(p.o.weight))
+    dst = p.spare.reshape(2, 4).copy()
+    dst[:, own] = p.table[:, own]
+    weight_out = p.c.weight if same_weights else torch.full_like(p.c.weight, 7.5)
+    kept = torch.zeros(2, 3, 250, dtype=torch.int32, device="cuda")
+    lens_out = torch.zeros(2, dtype=torch.int32, device="cuda")
+    ws = torch.full((sla.sla_cache_evict_workspace_bytes(p.cfg, 250),), 0xff, dtype=torch.uint8, device="cuda")
+    want_w = f64(weight_out)
+    sla.sla_cache_evict(p.cfg, p.c, i32(p.lens), 250, 2, 30, i32(dst), weight_out, kept, lens_out, ws)
+    p.status()
+    np.testing.assert_array_equal(kept.cpu().numpy(), p.o.evict(p.lens, 250, 2, 30, dst, want_w))
+    np.testing.assert_array_equal(f64(weight_out), want_w)
+    p.lens, p.o.weight = np.array([250, 250]), want_w
+    p.c.weight.copy_(weight_out)
+    p.check(dst)
+
+
 def test_evict_in_a_captured_graph():
     """Replayed twice on the same cache, other weights each time, in place and packed again."""
     p = Pair(B=2, H=2, H_kv=2, d=64, max_blocks=10, kind=INT8, spare=0, seed=37)
@@ -940,6 +964,71 @@ def test_evict_reports_bad_pages_and_lengths():
     p.status((sla.SLA_ERR_DEVICE_CHECK, 111))
     assert lens_out.tolist() == [0, 0, 0] and (kept == -1).all()
     assert torch.equal(p.c.k.view(torch.uint8), before)
+
+
+def test_calls_without_means_or_weights():
+    """k_mean and weight may be left out where a call does not need them."""
+    p = Pair(B=2, H=2, H_kv=2, d=64, max_blocks=4, spare=8, seed=44)
+    names = ("k", "v", "k_scale", "v_scale", "block_table", "status")
+    bare = sla.SlaCache(**{n: getattr(p.c, n) for n in names}, k_mean=None, weight=None)
+    weighted = sla.SlaCache(**{n: getattr(p.c, n) for n in names}, k_mean=None, weight=p.c.weight)
+    k, v = p.kv(200)
+    sla.sla_cache_append(k, v, p.cfg, bare, i32([0, 0]), i32([200, 100]))
+    p.lens = p.o.append(f64(k), f64(v), p.lens, [200, 100])
+    assert torch.isnan(p.c.k_mean).all() and torch.isnan(p.c.weight).all()
+    p.o.weight[:] = np.random.default_rng(1).random(p.o.weight.shape).astype(np.float32)
+    p.c.weight.copy_(torch.from_numpy(p.o.weight))
+    dst, want_w = p.spare[:6].reshape(2, 3), p.o.weight.copy()
+    kept = torch.zeros(2, 2, 130, dtype=torch.int32, device="cuda")
+    lens_out = torch.zeros(2, dtype=torch.int32, device="cuda")
+    ws = torch.empty(sla.sla_cache_evict_workspace_bytes(p.cfg, 130), dtype=torch.uint8, device="cuda")
+    sla.sla_cache_evict(p.cfg, weighted, i32(p.lens), 130, 1, 1, i32(dst), p.c.weight, kept, lens_out, ws)
+    p.status()
+    np.testing.assert_array_equal(kept.cpu().numpy(), p.o.evict(p.lens, 130, 1, 1, dst, want_w))
+    p.lens, p.o.weight = np.array([130, 100]), want_w
+    assert torch.isnan(p.c.k_mean).all()
+    p.o.mean[:] = np.nan
+    p.check(dst)
+    with pytest.raises(sla.SlaError):
+        sla.sla_cache_route(p.queries(1), p.cfg, bare, i32(p.lens), None, torch.zeros(2, 2, 1, dtype=torch.int32, device="cuda"))
+    with pytest.raises(sla.SlaError):
+        sla.sla_cache_evict(p.cfg, bare, i32(p.lens), 130, 1, 1, i32(dst), p.c.weight, kept, lens_out, ws)
+
+
+@pytest.mark.parametrize("H", [4, 132])
+def test_a_scale_of_the_callers(H):
+    p = Pair(B=2, H=H, H_kv=2, d=128, max_blocks=8, kind=INT8, scale=0.03, seed=45)
+    p.fill([500, 77])
+    q = p.queries(1, std=2.0)
+    p.check_attend(q)
+    want, gap = p.o.route(f64(q), p.lens, [1, 1], 3)
+    assert gap > 1e-9
+    np.testing.assert_array_equal(run_route(p, q, 3), want)
+
+
+@pytest.mark.parametrize("H,H_kv,d", [(2, 1, 128), (8, 2, 64), (66, 1, 64)])
+def test_the_most_sequences(H, H_kv, d):
+    """1024 sequences: their lengths alone are 9 KB of every attention CTA's shared memory."""
+    p = Pair(B=1024, H=H, H_kv=H_kv, d=d, max_blocks=2, kind=INT8, seed=46)
+    p.fill((np.arange(1024) * 7) % 129)
+    q = p.queries(1)
+    p.check_attend(q)
+    want, gap = p.o.route(f64(q), p.lens, np.ones(1024, int), 2)
+    assert gap > 1e-9
+    np.testing.assert_array_equal(run_route(p, q, 2), want)
+    p.o.weight[:] = np.random.default_rng(0).integers(0, 9, p.o.weight.shape)
+    p.c.weight.copy_(torch.from_numpy(p.o.weight))
+    dst, _ = run_evict(p, 70, 3, 20, True)
+    p.check(dst)
+
+
+@pytest.mark.parametrize("H_kv", [1, 1024])
+def test_the_most_heads(H_kv):
+    p = Pair(B=2, H=1024, H_kv=H_kv, d=64, max_blocks=2, seed=47)
+    p.fill([100, 65])
+    q = p.queries(1)
+    p.check_attend(q)
+    np.testing.assert_array_equal(run_route(p, q, 3), p.o.route(f64(q), p.lens, [1, 1], 3)[0])
 
 
 # ---------------------------------------------------------------------------
