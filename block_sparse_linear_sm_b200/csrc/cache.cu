@@ -697,7 +697,8 @@ sla_status sla_cache_evict(const sla_cache_config* cfg, const sla_cache* cache, 
   // slots: 60 us, 72 with 1024, whose 512 CTAs came in two waves). Up to 2048 slots one CTA is
   // no slower than eight (8 heads of 2048: 13 and 14 us), and up to 8192 it is faster where the
   // eights come in several waves (300 heads of 1025 slots 21 and 68 us, of 8192 104 and 124; 64
-  // heads of 8192, in one wave, 40 and 32).
+  // heads of 8192, in one wave, 40 and 32). The rule goes by the table's length, since the host
+  // does not know the sequences': short ones in a table of more than 8192 slots take eight CTAs.
   auto select = [&](auto kernel, int ctas, int threads, int most) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                select_run(most, ctas, threads) * (int)sizeof(uint32_t));

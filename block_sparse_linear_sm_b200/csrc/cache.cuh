@@ -28,7 +28,8 @@ struct CacheView {
 
 // Every kernel of the cache is launched so that it may start while the one before it in the
 // stream still runs (programmatic dependent launch): it sets itself up, waits for that one to
-// be complete before it touches global memory, and lets the next one start likewise.
+// be complete before it touches global memory (but see scan_lines), and lets the next one start
+// likewise.
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;"); }
 

@@ -28,11 +28,13 @@
 // What bounds it. A large batch: HBM (64 sequences of up to 16384 tokens, 8 KV heads, 4 rows
 // each: 189 us on the device for 1.25 GB, 6.6 TB/s, the measured copy rate; with the
 // rows as the 16-row operand, 4 rows padded to 16, it was 240). A few sequences: latency. A
-// warp's tile takes some 4000 cycles (products 1300 and 1500, softmax 1000), and 296 CTAs leave
-// it three or four tiles behind a start of 3 us (lengths, table, page): 65536 tokens of one
-// sequence, 16 rows, 20 us. More than 16 rows read a page once a group of 16, from L2: 128 rows
-// were bound by that (5.9 TB/s of L2 reads), hence the other kernel. Twelve warps an SM instead
-// of eight, at 168 registers, were 12 % slower.
+// warp's tile takes some 4000 cycles (products 1300 and 1500, softmax 1000, read from the clock in
+// an instrumented copy), and 296 CTAs leave it three or four tiles behind a start of 3 us
+// (lengths, table, page): 65536 tokens of one sequence, 16 rows, 20 us. More than 16 rows read a
+// page once a group of 16, from L2: 128 rows were bound by that (5.9 TB/s of L2 reads), hence
+// the other kernel. Twelve warps an SM instead of eight, at 168 registers, were 12 % slower. The
+// lengths of more than 650 sequences leave room for one CTA an SM instead of two (9 to 16 rows,
+// d 128): the second half of the CTAs then comes in a second wave.
 #include <cuda.h>
 
 #include <algorithm>

@@ -20,10 +20,12 @@
 // kernel for few rows. S and P are double buffered, so that the softmax of one page runs while
 // the products of the next are issued.
 // What bounds it: the row warps' chain, about 2600 cycles a page (maximum 450, exponentials 690,
-// P V 630, barriers and descriptions 700); the products need about 520 of them, the page's bytes
-// 710. 8 sequences of up to 16001 tokens, 4 KV heads, 128 rows: 66 us on the device. Splitting
-// the row work over two warpgroups, by pages (two outputs merged at the end) or by kind (softmax
-// apart from O), did not shorten it: each part then took almost twice as long.
+// P V 630, barriers and descriptions 700, read from the clock in an instrumented copy); the
+// products need about 520 of them, the page's bytes 710. 8 sequences of up to 16001 tokens, 4 KV
+// heads, 128 rows: 66 us on the device. No pipe is near full (profiles/cache_calls.md: tensor
+// 13 %, exponentials and conversions 16 %, 29 % of the issue slots). Splitting the row work over
+// two warpgroups, by pages (two outputs merged at the end) or by kind (softmax apart from O), did
+// not shorten it: each part then took almost twice as long, for a reason that was not found.
 #include "cache_attend.cuh"
 
 namespace sla {

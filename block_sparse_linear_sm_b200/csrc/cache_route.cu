@@ -14,10 +14,12 @@
 // means give equal sums wherever they are. A CTA sends its own top_n to the first one, which
 // picks the blocks that fewer than top_n of all those are ahead of.
 // Bound by its chain of dependent steps (lengths, table, means, three cluster barriers), not by
-// bytes; in large batches by fp64 instructions (64 a cycle and SM, tensor path or not). Remote
-// stores before a barrier instead of remote loads behind it, one exponential a score and
-// integer comparisons are what shortened it. 5000 tokens, 16 heads a KV head: 11 us; 16
-// sequences of up to 65536: 32 us.
+// bytes, and in large batches not by a pipe either: with 16 sequences of up to 65536 tokens
+// the fp64 pipe is 4 % busy, the tensor pipe 14 %, 30 % of the issue slots are taken, and warps
+// wait at barriers, for loads and for shared memory (profiles/cache_calls.md). Remote stores
+// before a barrier instead of remote loads behind it, one exponential a score and integer
+// comparisons are what shortened it. 5000 tokens, 16 heads a KV head: 11 us; 16 sequences of up
+// to 65536: 33 us.
 #include "cache.cuh"
 
 namespace sla {

@@ -523,8 +523,9 @@ SLA_API sla_status sla_cache_route(const void* q, const sla_cache_config* cfg, c
  * vary from run to run). Slots at lens[b] and beyond never count, whatever they hold. A
  * query row that holds a NaN or an infinity becomes NaN and adds no weight; other rows do
  * not notice.
- * Scores, maxima, sums and weights are fp32; for the product with V a probability is rounded
- * to fp16, 2^-11 of it, or 2^-33 of the row's largest where that is more.
+ * Scores, maxima, sums and weights are fp32 (a score beyond its range leaves its row undefined); for the
+ * product with V a probability is rounded to fp16, 2^-11 of it, or 2^-33 of the row's largest
+ * where that is more.
  * ws: sla_cache_attend_workspace_bytes bytes (with_weight: cache->weight is not NULL),
  * 256-byte aligned, needs no initialisation.
  */
@@ -554,6 +555,8 @@ SLA_API sla_status sla_cache_attend(const void* q, const sla_cache_config* cfg, 
  *               lens
  * A sequence of at most budget tokens moves unchanged to its dst_table pages. Full new
  * blocks get their k_mean (when kept). budget > 64 * max_blocks: SLA_ERR_INVALID_ARG.
+ * With the status word set: a length out of range counts as 0, tokens of a page whose number is
+ * out of range become 0, and a new block whose page number is out of range is not written.
  * ws: sla_cache_evict_workspace_bytes bytes, 256-byte aligned, needs no initialisation.
  */
 SLA_API size_t sla_cache_evict_workspace_bytes(const sla_cache_config* cfg, int32_t budget);
